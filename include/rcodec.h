@@ -203,6 +203,90 @@ rc_status rc_mxfp4_gemv(const void *w, size_t rows, size_t cols, rc_dtype x_t, c
  * the codec kernels are measured against. */
 rc_status rc_copy(const void *in, void *out, size_t bytes, void *stream);
 
+/* ---- Operators around the codec -------------------------------------------
+ *
+ * What stands next to a quantized all-reduce in a tensor-parallel model: the
+ * products on either side of it (grouped by expert, on MXFP4 weights), the
+ * norms between its result and the next block, and the norm and clipping of
+ * the gradients that were reduced.  The conventions above hold, with the
+ * additions named at each.  Sums are held in FP32 or FP64 and every output is
+ * rounded once, to nearest even. */
+
+#define RC_MAX_EXPERTS 65535
+#define RC_MAX_WIDTH 1048576
+
+/* Products grouped by expert.  W holds `experts` matrices of n x k, row-major,
+ * one after another, as one MXFP4 packed stream (rc_quantize_pack of their
+ * experts*n*k elements with {MXFP4, E8M0, 32}).  The rows of x (rows x k) are
+ * sorted by expert: expert e has rows offsets[e] <= i < offsets[e+1]; offsets
+ * is a device array of experts+1 ascending values in [0, rows].
+ *   rc_mxfp4_grouped_matmul     y[i] = W_e x[i]             y: rows x n
+ *   rc_mxfp4_grouped_matmul_dx  dx[i] = W_e^T dy[i]          dx: rows x k
+ *   rc_grouped_matmul_dw        dW[e] = sum_i dy[i] x[i]^T   dw: experts x n x k
+ * dW is dense: the gradient of the values that were cast to MXFP4, passed
+ * straight through the cast.  An expert without rows gets dW[e] = 0; rows of
+ * no expert (before offsets[0] or from offsets[experts] on) get y = dx = 0.
+ * Offsets that do not ascend or leave [0, rows] give unspecified results but
+ * no access outside the buffers.
+ * k must be a multiple of 32 (an MXFP4 block does not cross rows) and n one of
+ * 8, both at most RC_MAX_WIDTH, rows below 2^31, experts at most
+ * RC_MAX_EXPERTS, else RC_ERR_RANGE.  Products are exact and sums FP32 (the
+ * order is fixed by sizes and offsets, so calls repeat bit for bit): each sum
+ * s of N products p satisfies |s - sum p| <= (N + 3) 2^-23 sum |p|.  With fp16
+ * and fp32 rows an infinity may come out as NaN. */
+rc_status rc_mxfp4_grouped_matmul(const void *w, size_t experts, size_t n, size_t k, const int32_t *offsets,
+                                  rc_dtype x_t, const void *x, size_t rows, rc_dtype y_t, void *y, void *stream);
+rc_status rc_mxfp4_grouped_matmul_dx(const void *w, size_t experts, size_t n, size_t k, const int32_t *offsets,
+                                     rc_dtype dy_t, const void *dy, size_t rows, rc_dtype dx_t, void *dx,
+                                     void *stream);
+rc_status rc_grouped_matmul_dw(size_t experts, size_t n, size_t k, const int32_t *offsets, rc_dtype t,
+                               const void *dy, const void *x, size_t rows, rc_dtype dw_t, void *dw, void *stream);
+
+/* The norms around a block, with its gate and the scaled residual.  For each
+ * of `rows` rows of d elements (1 <= d <= 32768, else RC_ERR_RANGE):
+ *   u = post_w * y * ry,  ry = 1 / sqrt(mean(y^2) + eps)   (post_w NULL: u = y, ry = 1)
+ *   h = alpha * r + gate * u
+ *   z = pre_w * h * rh,   rh = 1 / sqrt(mean(h^2) + eps)   (h before rounding)
+ * y (the block's output), r (the residual stream), h, z: rows x d of type t;
+ * post_w, pre_w: d values of type w_t.  gate: none, d values of type w_t
+ * (RC_GATE_CHANNEL), or rows x d of type t (RC_GATE_FULL).  stats: NULL, or
+ * 2 x rows values, all ry then all rh, which the backward pass reads.  h may
+ * be r and z may be y (in place); no other overlap. */
+typedef enum { RC_GATE_NONE = 0, RC_GATE_CHANNEL = 1, RC_GATE_FULL = 2 } rc_gate;
+rc_status rc_block_norm(rc_dtype t, size_t rows, size_t d, const void *y, const void *r, rc_dtype w_t,
+                        const void *post_w, rc_gate gate_mode, const void *gate, const void *pre_w, float alpha,
+                        float eps, void *h, void *z, float *stats, void *stream);
+
+/* Its gradients, from dz, dh (the gradient that reaches h on other ways; NULL
+ * = 0), and the forward pass's y, h (as stored) and stats: dy and dr (rows x
+ * d, type t), dpre and dpost (d fp32 values; dpost unused without post_w),
+ * dgate (d fp32 values, or rows x d of type t; unused without a gate).  alpha
+ * is a constant.  dr may be dh and dy may be dz (in place).  rows = 0: the
+ * sums over rows are 0.  workspace: rc_block_norm_backward_workspace(rows, d) bytes of
+ * device memory, 16-byte aligned, written before it is read.  Sums over rows
+ * are added in an order that the sizes fix: calls repeat bit for bit. */
+size_t rc_block_norm_backward_workspace(size_t rows, size_t d);
+rc_status rc_block_norm_backward(rc_dtype t, size_t rows, size_t d, const void *dz, const void *dh, const void *h,
+                                 const float *stats, const void *y, rc_dtype w_t, const void *post_w,
+                                 rc_gate gate_mode, const void *gate, const void *pre_w, float alpha, void *dy,
+                                 void *dr, float *dpre, float *dpost, void *dgate, void *workspace, void *stream);
+
+/* Global norm of `count` tensors, and clipping by it:
+ *   N = |scale| sqrt(sum of all squares)   -> norm (one fp32 value)
+ *   out = g * scale * min(1, max_norm / (N + eps))
+ * for every tensor, rounded once to its out_t.  grads: HOST array, read before
+ * the call returns.  A tensor may be scaled in place (in == out, one type);
+ * otherwise inputs and outputs must not overlap.  Tensors need the alignment of
+ * their elements only (they may be parts of one buffer).  The squares are added
+ * in FP64 in an order that the sizes fix.  A norm that is infinite or NaN
+ * gives factors of 0 or NaN, as the formulas say.  max_norm or eps negative or
+ * NaN: RC_ERR_RANGE; max_norm = INFINITY: the norm alone and the scale.
+ * workspace: rc_grad_norm_clip_workspace() bytes, 16-byte aligned. */
+typedef struct { const void *in; void *out; uint64_t n; int32_t in_t, out_t; } rc_grad;
+size_t rc_grad_norm_clip_workspace(void);
+rc_status rc_grad_norm_clip(const rc_grad *grads, size_t count, float scale, float max_norm, float eps,
+                            void *workspace, float *norm, void *stream);
+
 /* Static description of a status code; never NULL. */
 const char *rc_status_str(rc_status s);
 

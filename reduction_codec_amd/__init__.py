@@ -12,9 +12,18 @@ Entry points (same names as the C ABI, minus the ``rc_`` prefix):
 * ``dequant_reduce_requant(streams, codec, n, sum_out=False)``
                                            -> (packed, fp32 sums or None)
 * ``tile_bytes(codec)``, ``packed_bytes(codec, n)``, ``copy(dst, src)``
+
+and the operators around a quantized all-reduce:
+
+* ``mxfp4_grouped_matmul(x, w_packed, offsets, n)``, ``mxfp4_grouped_matmul_dx``,
+  ``grouped_matmul_dw``               -> products grouped by expert
+* ``block_norm(y, residual, pre_weight, ...)``, ``block_norm_backward``
+                                           -> norms around a block, gate, residual
+* ``grad_norm_clip(grads, max_norm)``  -> global norm of many tensors, clipping
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -30,6 +39,7 @@ MAX_STREAMS = 16
 FMT_INT4, FMT_INT3, FMT_FP8_E4M3, FMT_MXFP4, FMT_FP8_E5M2 = 1, 2, 3, 4, 5
 SCALE_FP16, SCALE_FP32, SCALE_E8M0 = 1, 2, 3
 DT_FP32, DT_FP16, DT_BF16 = 1, 2, 3
+GATE_NONE, GATE_CHANNEL, GATE_FULL = 0, 1, 2
 OK, ERR_NULL, ERR_UNSUPPORTED, ERR_ALIGN, ERR_RANGE, ERR_HIP = 0, 1, 2, 3, 4, 5
 
 
@@ -95,6 +105,21 @@ def lib() -> ctypes.CDLL:
     l.rc_mxfp4_gemv.argtypes = [vp, sz, sz, i32, vp, i32, vp, vp]
     l.rc_allreduce_emulate.restype = i32
     l.rc_allreduce_emulate.argtypes = [Codec, i32, ctypes.POINTER(vp), i32, sz, i32, vp, vp, vp]
+    l.rc_mxfp4_grouped_matmul.restype = i32
+    l.rc_mxfp4_grouped_matmul.argtypes = [vp, sz, sz, sz, vp, i32, vp, sz, i32, vp, vp]
+    l.rc_mxfp4_grouped_matmul_dx.restype = i32
+    l.rc_mxfp4_grouped_matmul_dx.argtypes = [vp, sz, sz, sz, vp, i32, vp, sz, i32, vp, vp]
+    l.rc_grouped_matmul_dw.restype = i32
+    l.rc_grouped_matmul_dw.argtypes = [sz, sz, sz, vp, i32, vp, vp, sz, i32, vp, vp]
+    f32 = ctypes.c_float
+    l.rc_block_norm.restype = i32
+    l.rc_block_norm.argtypes = [i32, sz, sz, vp, vp, i32, vp, i32, vp, vp, f32, f32, vp, vp, vp, vp]
+    l.rc_block_norm_backward_workspace.restype, l.rc_block_norm_backward_workspace.argtypes = sz, [sz, sz]
+    l.rc_block_norm_backward.restype = i32
+    l.rc_block_norm_backward.argtypes = [i32, sz, sz, vp, vp, vp, vp, vp, i32, vp, i32, vp, vp, f32,
+                                         vp, vp, vp, vp, vp, vp, vp]
+    l.rc_grad_norm_clip_workspace.restype, l.rc_grad_norm_clip_workspace.argtypes = sz, []
+    l.rc_grad_norm_clip.restype, l.rc_grad_norm_clip.argtypes = i32, [vp, sz, f32, f32, f32, vp, vp, vp]
     l.rc_status_str.restype, l.rc_status_str.argtypes = ctypes.c_char_p, [i32]
     l.rc_abi_version.restype, l.rc_abi_version.argtypes = i32, []
     if l.rc_abi_version() != ABI_VERSION:
@@ -326,3 +351,239 @@ def copy(dst: torch.Tensor, src: torch.Tensor, stream=None) -> torch.Tensor:
     with torch.cuda.device(src.device):
         _ok(lib().rc_copy(src.data_ptr(), dst.data_ptr(), nbytes, hs), "rc_copy")
     return dst
+
+
+# ------------------------------------------- operators around the codec ----
+
+def _dtype(dt: torch.dtype, name: str) -> int:
+    if dt not in _DTYPES:
+        raise ValueError(f"unsupported {name} dtype {dt}")
+    return _DTYPES[dt]
+
+
+def _result(out, shape, dtype, like: torch.Tensor, stream, name: str) -> torch.Tensor:
+    """The caller's output, checked, or a new one for work on `stream`."""
+    if out is None:
+        return _mine(torch.empty(shape, dtype=dtype, device=like.device), stream)
+    _check_dev(out, name)
+    _same_device(like.device, (name, out))
+    if out.dtype != dtype or tuple(out.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
+    return out
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows_of(t: torch.Tensor, name: str, offsets: torch.Tensor):
+    _check_dev(t, name)
+    _check_dev(offsets, "offsets")
+    _same_device(t.device, ("offsets", offsets))
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, rows and width")
+    if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError("offsets must hold experts + 1 int32 values")
+    return t.shape[0], t.shape[1], offsets.numel() - 1
+
+
+def _weights(w_packed: torch.Tensor, experts: int, n: int, k: int, dev):
+    _check_dev(w_packed, "w_packed")
+    _same_device(dev, ("w_packed", w_packed))
+    if n < 0 or k < 0 or w_packed.dtype != torch.uint8 or w_packed.numel() < packed_bytes(MXFP4, experts * n * k):
+        raise ValueError("w_packed must hold packed_bytes(MXFP4, experts * n * k) bytes")
+
+
+def mxfp4_grouped_matmul(x: torch.Tensor, w_packed: torch.Tensor, offsets: torch.Tensor, n: int,
+                         out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+    """y[i] = W_e x[i] for the rows offsets[e] <= i < offsets[e + 1] of x
+    (rows x k, sorted by expert): W_e is n x k, all experts one after another
+    in one MXFP4 packed stream; offsets int32 on the GPU, experts + 1 values.
+    Returns rows x n of out_dtype (x's by default).  See
+    rc_mxfp4_grouped_matmul."""
+    rows, k, experts = _rows_of(x, "x", offsets)
+    _weights(w_packed, experts, n, k, x.device)
+    hs = _stream(stream, x.device)
+    y_t = x.dtype if out_dtype is None else out_dtype
+    xt, yt = _dtype(x.dtype, "x"), _dtype(y_t, "output")
+    out = _result(out, (rows, n), y_t, x, stream, "out")
+    with torch.cuda.device(x.device):
+        _ok(lib().rc_mxfp4_grouped_matmul(w_packed.data_ptr(), experts, n, k, offsets.data_ptr(), xt, x.data_ptr(),
+                                          rows, yt, out.data_ptr(), hs), "rc_mxfp4_grouped_matmul")
+    return out
+
+
+def mxfp4_grouped_matmul_dx(dy: torch.Tensor, w_packed: torch.Tensor, offsets: torch.Tensor, k: int,
+                            out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                            stream=None) -> torch.Tensor:
+    """dx[i] = W_e^T dy[i]: the gradient of mxfp4_grouped_matmul's rows, from
+    dy (rows x n); rows x k of out_dtype (dy's by default)."""
+    rows, n, experts = _rows_of(dy, "dy", offsets)
+    _weights(w_packed, experts, n, k, dy.device)
+    hs = _stream(stream, dy.device)
+    dx_t = dy.dtype if out_dtype is None else out_dtype
+    yt, xt = _dtype(dy.dtype, "dy"), _dtype(dx_t, "output")
+    out = _result(out, (rows, k), dx_t, dy, stream, "out")
+    with torch.cuda.device(dy.device):
+        _ok(lib().rc_mxfp4_grouped_matmul_dx(w_packed.data_ptr(), experts, n, k, offsets.data_ptr(), yt,
+                                             dy.data_ptr(), rows, xt, out.data_ptr(), hs),
+            "rc_mxfp4_grouped_matmul_dx")
+    return out
+
+
+def grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
+                      out_dtype: torch.dtype = torch.float32, out: torch.Tensor | None = None,
+                      stream=None) -> torch.Tensor:
+    """dW[e] = sum over expert e's rows of dy[i] x[i]^T (experts x n x k): the
+    dense gradient of the weights before their cast to MXFP4."""
+    rows, n, experts = _rows_of(dy, "dy", offsets)
+    _check_dev(x, "x")
+    _same_device(dy.device, ("x", x))
+    if x.dim() != 2 or x.shape[0] != rows or x.dtype != dy.dtype:
+        raise ValueError("x must have dy's rows and dtype")
+    k = x.shape[1]
+    hs = _stream(stream, dy.device)
+    t, wt = _dtype(dy.dtype, "dy"), _dtype(out_dtype, "output")
+    out = _result(out, (experts, n, k), out_dtype, dy, stream, "out")
+    with torch.cuda.device(dy.device):
+        _ok(lib().rc_grouped_matmul_dw(experts, n, k, offsets.data_ptr(), t, dy.data_ptr(), x.data_ptr(), rows, wt,
+                                       out.data_ptr(), hs), "rc_grouped_matmul_dw")
+    return out
+
+
+def _norm_weights(like: torch.Tensor, d: int, pre_weight, post_weight, gate):
+    """(weight type, gate mode) of a block norm; the gate is None, d values of
+    the weights' type, or one per element of `like`, of its type."""
+    for name, w in (("pre_weight", pre_weight), ("post_weight", post_weight), ("gate", gate)):
+        if w is not None:
+            _check_dev(w, name)
+            _same_device(like.device, (name, w))
+    wt = _dtype(pre_weight.dtype, "weight")
+    if pre_weight.numel() != d or (post_weight is not None and
+                                   (post_weight.numel() != d or post_weight.dtype != pre_weight.dtype)):
+        raise ValueError("pre_weight and post_weight must hold one value per column, of one dtype")
+    if gate is None:
+        return wt, GATE_NONE
+    if gate.dim() == 1 and gate.numel() == d and gate.dtype == pre_weight.dtype:
+        return wt, GATE_CHANNEL
+    if gate.shape == like.shape and gate.dtype == like.dtype:
+        return wt, GATE_FULL
+    raise ValueError("gate must be one value per column of the weights' dtype, or y's shape and dtype")
+
+
+def _like(t: torch.Tensor, like: torch.Tensor, name: str):
+    _check_dev(t, name)
+    _same_device(like.device, (name, t))
+    if t.shape != like.shape or t.dtype != like.dtype:
+        raise ValueError(f"{name} must have y's shape and dtype")
+
+
+def block_norm(y: torch.Tensor, residual: torch.Tensor, pre_weight: torch.Tensor,
+               post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+               residual_scale: float = 1.0, eps: float = 1e-6, stats: bool = False,
+               h: torch.Tensor | None = None, z: torch.Tensor | None = None, stream=None):
+    """Norm of a block's output y, its gate, the scaled residual and the norm
+    before the next block, over the last dimension:
+
+        u = post_weight * y / rms(y)  (u = y without post_weight)
+        h = residual_scale * residual + gate * u
+        z = pre_weight * h / rms(h)
+
+    Returns (h, z, stats): stats is None, or the 2 x rows fp32 values that
+    block_norm_backward reads.  h may be the residual and z may be y.  See
+    rc_block_norm."""
+    _check_dev(y, "y")
+    if y.dim() < 1 or y.shape[-1] == 0:
+        raise ValueError("y must have a last dimension of at least one value")
+    d = y.shape[-1]
+    rows = y.numel() // d
+    _like(residual, y, "residual")
+    wt, mode = _norm_weights(y, d, pre_weight, post_weight, gate)
+    t = _dtype(y.dtype, "y")
+    hs = _stream(stream, y.device)
+    h = _result(h, y.shape, y.dtype, y, stream, "h")
+    z = _result(z, y.shape, y.dtype, y, stream, "z")
+    st = _result(None, (2, rows), torch.float32, y, stream, "stats") if stats else None
+    with torch.cuda.device(y.device):
+        _ok(lib().rc_block_norm(t, rows, d, y.data_ptr(), residual.data_ptr(), wt, _ptr(post_weight), mode,
+                                _ptr(gate), pre_weight.data_ptr(), residual_scale, eps, h.data_ptr(), z.data_ptr(),
+                                _ptr(st), hs), "rc_block_norm")
+    return h, z, st
+
+
+def block_norm_backward(dz: torch.Tensor, dh: torch.Tensor | None, h: torch.Tensor, stats: torch.Tensor,
+                        y: torch.Tensor, pre_weight: torch.Tensor, post_weight: torch.Tensor | None = None,
+                        gate: torch.Tensor | None = None, residual_scale: float = 1.0,
+                        dy: torch.Tensor | None = None, dresidual: torch.Tensor | None = None, stream=None):
+    """Gradients of block_norm from dz and dh (what reaches h beside z, or
+    None), with the forward pass's y, h and stats.  Returns (dy, dresidual,
+    dpre, dpost, dgate); dpre, dpost and a channel gate's gradient are fp32, a
+    full gate's has y's dtype; dpost and dgate are None where there is no such
+    input.  dy may be dz and dresidual may be dh.  See rc_block_norm_backward."""
+    _check_dev(y, "y")
+    if y.dim() < 1 or y.shape[-1] == 0:
+        raise ValueError("y must have a last dimension of at least one value")
+    d = y.shape[-1]
+    rows = y.numel() // d
+    for name, g in (("dz", dz), ("h", h)) + ((("dh", dh),) if dh is not None else ()):
+        _like(g, y, name)
+    _check_dev(stats, "stats")
+    _same_device(y.device, ("stats", stats))
+    if stats.dtype != torch.float32 or stats.numel() != 2 * rows:
+        raise ValueError("stats must hold 2 x rows float32 values")
+    wt, mode = _norm_weights(y, d, pre_weight, post_weight, gate)
+    t = _dtype(y.dtype, "y")
+    hs = _stream(stream, y.device)
+    dy = _result(dy, y.shape, y.dtype, y, stream, "dy")
+    dr = _result(dresidual, y.shape, y.dtype, y, stream, "dresidual")
+    new = lambda shape, dt: _mine(torch.empty(shape, dtype=dt, device=y.device), stream)  # noqa: E731
+    dpre = new((d,), torch.float32)
+    dpost = new((d,), torch.float32) if post_weight is not None else None
+    dgate = None if gate is None else new((d,), torch.float32) if mode == GATE_CHANNEL else new(y.shape, y.dtype)
+    ws = new((lib().rc_block_norm_backward_workspace(rows, d),), torch.uint8)
+    with torch.cuda.device(y.device):
+        _ok(lib().rc_block_norm_backward(t, rows, d, dz.data_ptr(), _ptr(dh), h.data_ptr(), stats.data_ptr(),
+                                         y.data_ptr(), wt, _ptr(post_weight), mode, _ptr(gate),
+                                         pre_weight.data_ptr(), residual_scale, dy.data_ptr(), dr.data_ptr(),
+                                         dpre.data_ptr(), _ptr(dpost), _ptr(dgate), ws.data_ptr(), hs),
+            "rc_block_norm_backward")
+    return dy, dr, dpre, dpost, dgate
+
+
+def grad_norm_clip(grads, max_norm: float, scale: float = 1.0, eps: float = 1e-6, out=None,
+                   norm: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Global norm N = |scale| * sqrt(sum of squares) of all the tensors
+    (bf16 / fp16 / fp32, mixed, any shapes and alignments), and every tensor
+    times scale * min(1, max_norm / (N + eps)): in place, or into the tensors
+    of `out` (same sizes, any of the types).  Returns N, one fp32 value on the
+    GPU; nothing waits for it.  See rc_grad_norm_clip."""
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if not grads:
+        raise ValueError("need at least one tensor")
+    if len(outs) != len(grads):
+        raise ValueError("out must hold one tensor for each of grads")
+    dev = grads[0].device
+    desc = array.array("Q")
+    for j, (g, o) in enumerate(zip(grads, outs)):
+        _check_dev(g, f"grads[{j}]")
+        if o is not g:
+            _check_dev(o, f"out[{j}]")
+            if o.numel() != g.numel():
+                raise ValueError(f"out[{j}] must hold as many values as grads[{j}]")
+        _same_device(dev, (f"grads[{j}]", g), (f"out[{j}]", o))
+        desc.extend((g.data_ptr(), o.data_ptr(), g.numel(),
+                     _dtype(g.dtype, "gradient") | _dtype(o.dtype, "output") << 32))
+    hs = _stream(stream, dev)
+    if norm is None:
+        norm = _mine(torch.empty(1, dtype=torch.float32, device=dev), stream)
+    _check_dev(norm, "norm")
+    _same_device(dev, ("norm", norm))
+    if norm.dtype != torch.float32 or norm.numel() < 1:
+        raise ValueError("norm must hold one float32 value")
+    ws = _mine(torch.empty(lib().rc_grad_norm_clip_workspace(), dtype=torch.uint8, device=dev), stream)
+    with torch.cuda.device(dev):
+        _ok(lib().rc_grad_norm_clip(desc.buffer_info()[0], len(grads), scale, max_norm, eps, ws.data_ptr(),
+                                    norm.data_ptr(), hs), "rc_grad_norm_clip")
+    return norm
