@@ -37,8 +37,8 @@ rc_status rc_mxfp4_grouped_matmul(const void* w, size_t experts, size_t n, size_
     if (s != RC_OK || rows == 0) return s;
     if (!w || !offsets || !x || !y) return RC_ERR_NULL;
     if (!aligned16(w) || !aligned16(offsets) || !aligned16(x) || !aligned16(y)) return RC_ERR_ALIGN;
-    const rc::Grouped g = {x, nullptr, static_cast<const uint8_t*>(w), offsets, y, rows, (int64_t)n, (int64_t)k, (int)experts};
-    return from_hip(rc::launch_grouped_forward(x_t, y_t, g, static_cast<hipStream_t>(stream)));
+    const rc::Grouped g = {x, nullptr, static_cast<const uint8_t*>(w), offsets, y, rows, (int64_t)n, (int64_t)k, (int)experts, y_t};
+    return from_hip(rc::launch_grouped_forward(x_t, g, static_cast<hipStream_t>(stream)));
 }
 
 rc_status rc_mxfp4_grouped_matmul_dx(const void* w, size_t experts, size_t n, size_t k, const int32_t* offsets,
@@ -49,8 +49,8 @@ rc_status rc_mxfp4_grouped_matmul_dx(const void* w, size_t experts, size_t n, si
     if (s != RC_OK || rows == 0) return s;
     if (!w || !offsets || !dy || !dx) return RC_ERR_NULL;
     if (!aligned16(w) || !aligned16(offsets) || !aligned16(dy) || !aligned16(dx)) return RC_ERR_ALIGN;
-    const rc::Grouped g = {dy, nullptr, static_cast<const uint8_t*>(w), offsets, dx, rows, (int64_t)n, (int64_t)k, (int)experts};
-    return from_hip(rc::launch_grouped_dx(dy_t, dx_t, g, static_cast<hipStream_t>(stream)));
+    const rc::Grouped g = {dy, nullptr, static_cast<const uint8_t*>(w), offsets, dx, rows, (int64_t)n, (int64_t)k, (int)experts, dx_t};
+    return from_hip(rc::launch_grouped_dx(dy_t, g, static_cast<hipStream_t>(stream)));
 }
 
 rc_status rc_grouped_matmul_dw(size_t experts, size_t n, size_t k, const int32_t* offsets, rc_dtype t,
@@ -61,8 +61,8 @@ rc_status rc_grouped_matmul_dw(size_t experts, size_t n, size_t k, const int32_t
     if (s != RC_OK) return s;
     if (!offsets || !dw || (rows != 0 && (!dy || !x))) return RC_ERR_NULL;
     if (!aligned16(offsets) || !aligned16(dw) || !aligned16(dy) || !aligned16(x)) return RC_ERR_ALIGN;
-    const rc::Grouped g = {dy, x, nullptr, offsets, dw, rows, (int64_t)n, (int64_t)k, (int)experts};
-    return from_hip(rc::launch_grouped_dw(t, dw_t, g, static_cast<hipStream_t>(stream)));
+    const rc::Grouped g = {dy, x, nullptr, offsets, dw, rows, (int64_t)n, (int64_t)k, (int)experts, dw_t};
+    return from_hip(rc::launch_grouped_dw(t, g, static_cast<hipStream_t>(stream)));
 }
 
 rc_status rc_block_norm(rc_dtype t, size_t rows, size_t d, const void* y, const void* r, rc_dtype w_t,

@@ -53,7 +53,7 @@ hipError_t launch_block_norm_backward(int dt, const BlockNormBackward& a, hipStr
 
 // ---- products grouped by expert (rc_op_experts.hip)
 // a: x (forward) or dy, of type dt; b: x (weight gradient only); w: packed
-// weights (not for the weight gradient); out of type ot.
+// weights (not for the weight gradient); out of type out_t.
 struct Grouped {
     const void *a, *b;
     const uint8_t* w;
@@ -61,10 +61,10 @@ struct Grouped {
     void* out;
     size_t rows;
     int64_t n, k;
-    int experts;
+    int experts, out_t;
 };
-hipError_t launch_grouped_forward(int dt, int ot, const Grouped& a, hipStream_t st);
-hipError_t launch_grouped_dx(int dt, int ot, const Grouped& a, hipStream_t st);
-hipError_t launch_grouped_dw(int dt, int ot, const Grouped& a, hipStream_t st);
+hipError_t launch_grouped_forward(int dt, const Grouped& a, hipStream_t st);
+hipError_t launch_grouped_dx(int dt, const Grouped& a, hipStream_t st);
+hipError_t launch_grouped_dw(int dt, const Grouped& a, hipStream_t st);
 
 }  // namespace rc
