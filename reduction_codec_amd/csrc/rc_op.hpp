@@ -15,6 +15,14 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16_pair __attribute__((ext_vector_type(2)));
 typedef _Float16 f16_pair __attribute__((ext_vector_type(2)));
 
+// A buffer descriptor for `bytes` bytes at base + off: offsets past them read
+// as zeros and move nothing.
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+__device__ __forceinline__ Rsrc span_rsrc(const void* base, size_t off, uint32_t bytes)
+{
+    return __builtin_amdgcn_make_buffer_rsrc((void*)(static_cast<const uint8_t*>(base) + off), (short)0, (int)bytes, 0x00020000);
+}
+
 template <int DT> struct Elem { static constexpr int size = (DT == kF32) ? 4 : 2, per16 = 16 / size; };
 
 // The elements of 16 bytes, widened exactly.

@@ -8,13 +8,15 @@
 // The matrix cores multiply bfloat16: every value that an E2M1 code and an
 // E8M0 scale stand for is a bfloat16 (subnormals and overflow to infinity
 // included), so weights are decoded without rounding.  Rows in fp16 and fp32
-// are cut into P = 2 and 3 bfloat16 terms that add up to them (fp16 exactly,
-// fp32 to 2^-24), one product per term; all sums are binary32.
+// are cut into P = 2 and 3 bfloat16 terms that add up to them exactly, one
+// product per term (dW in fp32: the six products of two terms that reach
+// 2^-22 of the whole; fp16 is multiplied as it is); all sums are binary32.
 //
 // The groups' bounds are read by the kernels: a tile index is mapped to its
 // expert by a wave-wide scan of the bounds, and a grid for the largest number
 // of tiles that the sizes allow is launched (surplus workgroups end at once).
 // Bounds are clamped to the rows there are, so no bounds can reach outside.
+#include <algorithm>
 #include "rc_op.hpp"
 #include "rc_op_launch.hpp"
 
@@ -28,7 +30,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr size_t kMaxGrid = 0x7FFFFFFF;          // workgroups of a launch
 
-enum : int { kFwd = 0, kDx = 1, kDw = 2 };
+enum : int { kDx = 1, kDw = 2 };
 
 template <int DT> struct Terms { static constexpr int v = DT == kBF16 ? 1 : DT == kF16 ? 2 : 3; };
 
@@ -65,37 +67,20 @@ __device__ __forceinline__ bool find_tile(const int32_t* off, int experts, int64
         const uint64_t past = __builtin_amdgcn_ballot_w64(before + upto > tile);
         if (past) {
             const int l = __builtin_ctzll(past);
-            const int64_t first = before + __shfl(upto - mine, l, 64);
-            seg = s0 + l;
-            row = (int64_t)__shfl(g.lo, l, 64) + (tile - first) * BM;
-            end = (int64_t)__shfl(g.hi, l, 64);
+            const int64_t first = before + __builtin_amdgcn_readlane(upto - mine, l);
+            seg = __builtin_amdgcn_readfirstlane(s0 + l);       // wave-uniform, in scalar registers; rows < 2^31
+            row = __builtin_amdgcn_readlane((int)g.lo, l) + (tile - first) * BM;
+            end = __builtin_amdgcn_readlane((int)g.hi, l);
             return true;
         }
-        before += __shfl(upto, 63, 64);
+        before += __builtin_amdgcn_readlane(upto, 63);
     }
     return false;
 }
 
-// v as P bfloat16 terms, the largest first: each is what is left, rounded
-// (cut, where rounding would reach infinity).  An infinity or a NaN is all in
-// the first term.
-template <int P>
-__device__ __forceinline__ void split(float v, uint16_t (&t)[P])
-{
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-        t[p] = (uint16_t)narrow2<kBF16>(v, 0.0f);
-        if (p + 1 < P) {
-            const bool finite = __builtin_fabsf(v) < __builtin_inff();
-            if (finite && (t[p] & 0x7FFF) == 0x7F80) t[p] = (uint16_t)(__float_as_uint(v) >> 16);
-            v = finite ? v - __uint_as_float((uint32_t)t[p] << 16) : 0.0f;
-        }
-    }
-}
-
-// ---- the tile kernel ---------------------------------------------------
+// ---- gradients: the tile kernel ----------------------------------------
 //
-// A BM x BN tile of the result per workgroup of WM x WN waves, BK = 64 of the
+// A BM x BN tile of the result per workgroup of WM x WN waves, BK of the
 // contracted dimension at a time.  Both operands pass through LDS, two buffers
 // of each: while the matrix cores work on one, the next step's global loads
 // are in flight to registers; they are decoded (weights), cut into terms (fp16
@@ -103,18 +88,17 @@ __device__ __forceinline__ void split(float v, uint16_t (&t)[P])
 // barrier ends the step.
 //
 // An operand lies in LDS as its memory has it: "row" (contraction innermost:
-// the rows and, forward, the weights), read with 16-byte loads; or "column"
-// (contraction outermost: the weights for dx, both operands of dW), read with
-// the transposing loads, which give lane i column i of four rows.  Both are
-// swizzled (row_at, col_at) so that the lanes of one load fall on all banks.
+// dy for dx), read with 16-byte loads; or "column" (contraction outermost: the
+// weights for dx, both operands of dW), read with the transposing loads, which
+// give lane i column i of four rows.  Both are swizzled (row_at, col_at) so
+// that the lanes of one load fall on all banks.
 //
-// The products are formed as weights x rows, so a lane's four results are
-// neighbours in the output's row and are stored together.
+// The products are formed with the tile's columns as the first operand, so a
+// lane's four results are neighbours in the output's row and are stored
+// together.
 
-constexpr int kBK = 64;
-
-// Byte offset of 16-byte unit c (eight contraction values) of row r.
-__device__ __forceinline__ uint32_t row_at(uint32_t r, uint32_t c) { return r * (kBK * 2) + ((c ^ (r >> 1 & 7)) << 4); }
+// Byte offset of 16-byte unit c (eight contraction values) of row r; BK = 64.
+__device__ __forceinline__ uint32_t row_at(uint32_t r, uint32_t c) { return r * 128 + ((c ^ (r >> 1 & 7)) << 4); }
 // Byte offset of unit c (eight columns) of contraction row r of `cols` columns.
 template <int COLS>
 __device__ __forceinline__ uint32_t col_at(uint32_t r, uint32_t c)
@@ -135,12 +119,13 @@ __device__ __forceinline__ Unit<DT> load_unit(const uint8_t* p, bool in)
     return u;
 }
 
-// The unit's P planes (terms), `plane` bytes apart in LDS.
+// Eight values of a row as P bfloat16 terms that add up to them exactly: the
+// leading eight bits cut off, then (fp32) the next eight rounded, then the rest.
 template <int DT, int P>
-__device__ __forceinline__ void store_unit(uint8_t* lds, uint32_t plane, const Unit<DT>& u)
+__device__ __forceinline__ void cut_unit(const Unit<DT>& u, u32x4 (&t)[P])
 {
     if constexpr (P == 1) {
-        *reinterpret_cast<u32x4*>(lds) = u.v[0];
+        t[0] = u.v[0];
     } else {
         float v[8];
         if constexpr (DT == kF32) {
@@ -149,18 +134,29 @@ __device__ __forceinline__ void store_unit(uint8_t* lds, uint32_t plane, const U
         } else {
             widen8<DT>(u.v[0], v);
         }
-        u32x4 t[P];
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-            uint16_t a[P], b[P];
-            split<P>(v[e], a);
-            split<P>(v[e + 1], b);
+            uint32_t w = __builtin_amdgcn_perm(__float_as_uint(v[e + 1]), __float_as_uint(v[e]), 0x07060302u);
 #pragma unroll
-            for (int p = 0; p < P; ++p) t[p][e / 2] = (uint32_t)a[p] | (uint32_t)b[p] << 16;
+            for (int p = 0; p < P; ++p) {
+                t[p][e / 2] = w;
+                if (p + 1 == P) break;
+                v[e] -= bf16lo(w);
+                v[e + 1] -= bf16hi(w);
+                w = narrow2<kBF16>(v[e], v[e + 1]);
+            }
         }
-#pragma unroll
-        for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4*>(lds + p * plane) = t[p];
     }
+}
+
+// The unit's P planes (terms), `plane` bytes apart in LDS.
+template <int DT, int P>
+__device__ __forceinline__ void store_unit(uint8_t* lds, uint32_t plane, const Unit<DT>& u)
+{
+    u32x4 t[P];
+    cut_unit<DT, P>(u, t);
+#pragma unroll
+    for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4*>(lds + p * plane) = t[p];
 }
 
 // One block of 32 weights: its codes and its scale.
@@ -220,15 +216,16 @@ template <int DIR, int DT> struct Planes {
     static constexpr int a = (DIR == kDw && DT == kF16) ? 1 : Terms<DT>::v, b = DIR == kDw ? a : 1;
 };
 
-template <int DIR, int DT, int BM, int BN, int WM, int WN>
+template <int DIR, int DT, int BM, int BN, int WM, int WN, int BK = 64>
 __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Grouped a, unsigned cols)
 {
     constexpr int T = 64 * WM * WN, PA = Planes<DIR, DT>::a, PB = Planes<DIR, DT>::b;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;                 // a wave's fragments
     constexpr bool F16 = DIR == kDw && DT == kF16;
-    constexpr uint32_t A_PLANE = BM * kBK * 2, B_PLANE = BN * kBK * 2;
-    constexpr int UA = BM * kBK / 8 / T, UB = BN * kBK / (DIR == kDw ? 8 : 32) / T;   // units, or blocks, of a lane
-    static_assert(UA >= 1 && UB >= 1 && UA * 8 * T == BM * kBK, "tile and threads");
+    constexpr uint32_t A_PLANE = BM * BK * 2, B_PLANE = BN * BK * 2;
+    constexpr int UA = BM * BK / 8 / T, UB = BN * BK / (DIR == kDw ? 8 : 32) / T;   // units, or blocks, of a lane
+    static_assert(UA >= 1 && UB >= 1 && UA * 8 * T == BM * BK, "tile and threads");
+    static_assert(DIR == kDw || BK == 64, "row operands");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr uint32_t BUF = PA * A_PLANE + PB * B_PLANE;
 
@@ -238,7 +235,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
     constexpr int ES = Elem<DT>::size;
     int seg;
     int64_t row, end, depth, m_end;              // the tile's first row, the group's end, the contraction's length
-    const int64_t col = (int64_t)(blockIdx.x % cols) * BN, n_end = DIR == kFwd ? nn : kk;
+    const int64_t col = (int64_t)(blockIdx.x % cols) * BN, n_end = kk;
     if constexpr (DIR == kDw) {
         const unsigned rt = (unsigned)((nn + BM - 1) / BM), t = blockIdx.x / cols;
         seg = (int)(t / rt) + 1;
@@ -248,7 +245,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
     } else {
         if (!find_tile<BM>(a.offsets, a.experts, a.rows, blockIdx.x / cols, seg, row, end)) return;
         m_end = end;
-        depth = (seg == 0 || seg > a.experts) ? 0 : DIR == kFwd ? kk : nn;   // rows of no expert: zeros
+        depth = (seg == 0 || seg > a.experts) ? 0 : nn;   // rows of no expert: zeros
     }
     const size_t wbase = (size_t)(seg - 1) * nn * kk;
     f32x4 acc[FM][FN];
@@ -266,7 +263,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
                 ra[i] = load_unit<DT>(static_cast<const uint8_t*>(a.a) + ((size_t)(end + c0 + r) * nn + row + c * 8) * ES,
                                       c0 + r < depth && row + c * 8 < nn);
             } else {
-                const uint32_t r = s / (kBK / 8), c = s % (kBK / 8);
+                const uint32_t r = s / (BK / 8), c = s % (BK / 8);
                 ra[i] = load_unit<DT>(static_cast<const uint8_t*>(a.a) + ((size_t)(row + r) * depth + c0 + c * 8) * ES,
                                       row + r < m_end && c0 + c * 8 < depth);
             }
@@ -278,10 +275,6 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
                 const uint32_t r = s / (BN / 8), c = s % (BN / 8);
                 rb[i] = load_unit<DT>(static_cast<const uint8_t*>(a.b) + ((size_t)(end + c0 + r) * kk + col + c * 8) * ES,
                                       c0 + r < depth && col + c * 8 < kk);
-            } else if constexpr (DIR == kFwd) {  // block c of W[col + r], from contraction c0 on
-                const uint32_t r = s / (kBK / 32), c = s % (kBK / 32);
-                rw[i] = load_block32(a.w, (int64_t)((wbase + (size_t)(col + r) * kk + c0) / 32 + c),
-                                     col + r < nn && c0 + c * 32 < kk);
             } else {                             // block c of W[c0 + r], from column col on
                 const uint32_t r = s / (BN / 32), c = s % (BN / 32);
                 rw[i] = load_block32(a.w, (int64_t)((wbase + (size_t)(c0 + r) * kk + col) / 32 + c),
@@ -294,7 +287,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
         for (int i = 0; i < UA; ++i) {
             const uint32_t s = i * T + tid;
             if constexpr (DIR == kDw) store_unit<DT, PA>(buf + col_at<BM>(s / (BM / 8), s % (BM / 8)), A_PLANE, ra[i]);
-            else store_unit<DT, PA>(buf + row_at(s / (kBK / 8), s % (kBK / 8)), A_PLANE, ra[i]);
+            else store_unit<DT, PA>(buf + row_at(s / (BK / 8), s % (BK / 8)), A_PLANE, ra[i]);
         }
         buf += PA * A_PLANE;
 #pragma unroll
@@ -306,8 +299,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
                 const float scale = __uint_as_float(rw[i].scale << 23);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t at = DIR == kFwd ? row_at(s / (kBK / 32), s % (kBK / 32) * 4 + e)
-                                                    : col_at<BN>(s / (BN / 32), s % (BN / 32) * 4 + e);
+                    const uint32_t at = col_at<BN>(s / (BN / 32), s % (BN / 32) * 4 + e);
                     *reinterpret_cast<u32x4*>(buf + at) = decode8(rw[i].codes[e], scale);
                 }
             }
@@ -322,28 +314,27 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
         if constexpr (DIR == kDw) at_col_a[f] = col_at<BM>(8 * q + m / 4, (wm * (BM / WM) + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
 #pragma unroll
     for (int f = 0; f < FN; ++f)
-        if constexpr (DIR != kFwd) at_col_b[f] = col_at<BN>(8 * q + m / 4, (wn * (BN / WN) + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
+        at_col_b[f] = col_at<BN>(8 * q + m / 4, (wn * (BN / WN) + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
     auto products = [&](const uint8_t* buf) {
 #pragma unroll
-        for (int s = 0; s < kBK / 32; ++s) {
+        for (int s = 0; s < BK / 32; ++s) {
 #pragma unroll
             for (int pb = 0; pb < PB; ++pb) {
                 u32x4 fb[FN];
 #pragma unroll
                 for (int f = 0; f < FN; ++f) {
                     const uint8_t* p = buf + PA * A_PLANE + pb * B_PLANE;
-                    if constexpr (DIR == kFwd) fb[f] = *reinterpret_cast<const u32x4*>(p + at_row[s] + (wn * (BN / WN) + 16 * f) * (kBK * 2));
-                    else fb[f] = load_columns(p + at_col_b[f] + s * 32 * BN * 2, 4 * BN * 2);
+                    fb[f] = load_columns(p + at_col_b[f] + s * 32 * BN * 2, 4 * BN * 2);
                 }
 #pragma unroll
                 for (int pa = 0; pa < PA; ++pa) {
-                    if (pa + pb > 2) continue;   // below 2^-24 of the product
+                    if (pa + pb > 2) continue;   // below 2^-22 of the product
                     u32x4 fa[FM];
 #pragma unroll
                     for (int f = 0; f < FM; ++f) {
                         const uint8_t* p = buf + pa * A_PLANE;
                         if constexpr (DIR == kDw) fa[f] = load_columns(p + at_col_a[f] + s * 32 * BM * 2, 4 * BM * 2);
-                        else fa[f] = *reinterpret_cast<const u32x4*>(p + at_row[s] + (wm * (BM / WM) + 16 * f) * (kBK * 2));
+                        else fa[f] = *reinterpret_cast<const u32x4*>(p + at_row[s] + (wm * (BM / WM) + 16 * f) * (BK * 2));
                     }
 #pragma unroll
                     for (int i = 0; i < FM; ++i)
@@ -358,9 +349,9 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
         store(lds);
         __syncthreads();
         uint32_t cur = 0;
-        for (int64_t c0 = 0; c0 < depth; c0 += kBK) {
-            const bool more = c0 + kBK < depth;
-            if (more) load(c0 + kBK);
+        for (int64_t c0 = 0; c0 < depth; c0 += BK) {
+            const bool more = c0 + BK < depth;
+            if (more) load(c0 + BK);
             products(lds + cur);
             cur ^= BUF;
             if (more) store(lds + cur);
@@ -380,16 +371,349 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
     }
 }
 
-template <int DIR, int DT, int BM, int BN, int WM, int WN>
+// ---- few rows per expert ------------------------------------------------
+//
+// Forward with a handful of rows per expert is bound by the weights' bytes, so
+// they go from memory straight to the registers that feed the matrix cores.
+// A workgroup forms 16 MF rows by 16 NF columns; its KW waves take every KW-th
+// span of 512 of the contracted dimension and add up through LDS in the waves'
+// order.  For 16 weight rows, lane (m, q) loads block q of four neighbours (64
+// contiguous bytes of a row); one exchange among the four q of a row gives it
+// eight codes of each of the four blocks, as the matrix instructions take them
+// (contraction values 8 q .. 8 q + 7 of a block), so that the rows' values are
+// read 64 contiguous bytes at a time too.
+
+// Word i of lane row q (of 16 lanes) to word q of lane row i.
+__device__ __forceinline__ u32x4 exchange(u32x4 c)
+{
+    const auto a = __builtin_amdgcn_permlane32_swap(c.x, c.z, false, false), b = __builtin_amdgcn_permlane32_swap(c.y, c.w, false, false);
+    const auto e = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false), o = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    return u32x4{(uint32_t)e[0], (uint32_t)e[1], (uint32_t)o[0], (uint32_t)o[1]};
+}
+
+// v[i] = the value that lane row i holds, in every lane row.
+__device__ __forceinline__ void spread(uint32_t x, uint32_t (&v)[4])
+{
+    const auto a = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    const auto e = __builtin_amdgcn_permlane16_swap(a[0], a[0], false, false), o = __builtin_amdgcn_permlane16_swap(a[1], a[1], false, false);
+    v[0] = e[0]; v[1] = e[1]; v[2] = o[0]; v[3] = o[1];
+}
+
+template <int DT, int MF, int NF, int KW, bool SPANS>
+__global__ __launch_bounds__(64 * KW) void grouped_thin_kernel(const Grouped a, unsigned cols)
+{
+    constexpr int P = Terms<DT>::v, ES = Elem<DT>::size, RU = DT == kF32 ? 2 : 1;
+    constexpr uint32_t kOut = 0xFFFFFF00u;           // past every descriptor's end: reads as zeros, moves nothing
+    __shared__ f32x4 part[KW][NF * MF][64];
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, m = lane & 15, q = lane >> 4;
+    const int64_t nn = a.n, kk = a.k, col = (int64_t)(blockIdx.x % cols) * (16 * NF);
+    const uint32_t blocks = (uint32_t)(kk / 32);
+    int seg;
+    int64_t row, end;
+    if (!find_tile<16 * MF>(a.offsets, a.experts, a.rows, blockIdx.x / cols, seg, row, end)) return;
+    const bool none = seg == 0 || seg > a.experts;   // rows of no expert: zeros
+    // the workgroup's weight rows and rows, each through one buffer descriptor with 32-bit offsets
+    const int64_t fb = ((int64_t)(seg - 1) * nn + col) * blocks;
+    const uint32_t wrows = (uint32_t)(nn - col < 16 * NF ? nn - col : 16 * NF), skip = (uint32_t)(fb & 63);
+    const uint32_t xrows = (uint32_t)(end - row < 16 * MF ? end - row : 16 * MF);
+    const Rsrc wr = span_rsrc(a.w, none ? 0 : (size_t)(fb >> 6) * 1088, none ? 0 : (skip + wrows * blocks + 63) / 64 * 1088);
+    const Rsrc xr = span_rsrc(a.a, (size_t)row * kk * ES, xrows * (uint32_t)kk * ES);
+    uint32_t first[NF];                              // the lane's weight rows' first blocks
+#pragma unroll
+    for (int f = 0; f < NF; ++f) first[f] = 16 * f + m < wrows ? skip + (16 * f + m) * blocks : kOut;
+    f32x4 acc[NF][MF];
+#pragma unroll
+    for (int i = 0; i < NF * MF; ++i) acc[i / MF][i % MF] = f32x4{0, 0, 0, 0};
+
+    struct Span { u32x4 codes[NF][4]; uint32_t scale[NF][4]; };
+    // blocks b0 + q, + 4, + 8, + 12 of the lane's weight rows (zeros past the row's end)
+    auto load_weights = [&](Span& w, uint32_t b0) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            if constexpr (SPANS) {
+                const uint32_t at = first[f] + b0;
+                const uint32_t tile = (first[f] == kOut || b0 >= blocks) ? kOut : (at >> 6) * 1088, in = at & 63;
+                const u32x4 sc = __builtin_amdgcn_raw_buffer_load_b128(wr, tile == kOut ? kOut : tile + 1024 + in, 0, 0);
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    w.codes[f][s] = __builtin_amdgcn_raw_buffer_load_b128(wr, tile == kOut ? kOut : tile + (in + q + 4 * s) * 16, 0, 0);
+                    w.scale[f][s] = sc[s];
+                }
+            } else {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) {
+                    const uint32_t b = b0 + q + 4 * s, at = first[f] + b;
+                    const bool in = first[f] != kOut && b < blocks;
+                    w.codes[f][s] = __builtin_amdgcn_raw_buffer_load_b128(wr, in ? (at >> 6) * 1088 + (at & 63) * 16 : kOut, 0, 0);
+                    w.scale[f][s] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(wr, in ? (at >> 6) * 1088 + 1024 + (at & 63) : kOut, 0, 0);
+                }
+            }
+        }
+    };
+    Unit<DT> u[4][MF][4];
+    auto load_rows = [&](uint32_t b0) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t b = b0 + 4 * s + j, at = ((16 * i + m) * (uint32_t)kk + b * 32 + 8 * q) * ES;
+                    const uint32_t off = (16 * i + m < xrows && b < blocks) ? at : kOut;
+#pragma unroll
+                    for (int h = 0; h < RU; ++h) u[s][i][j].v[h] = __builtin_amdgcn_raw_buffer_load_b128(xr, off + 16 * h, 0, 0);
+                }
+    };
+    auto products = [&](const Span& w) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            u32x4 codes[NF];
+            uint32_t scale[NF][4];
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                codes[f] = exchange(w.codes[f][s]);
+                if constexpr (SPANS) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) scale[f][j] = w.scale[f][s] >> (8 * j) & 255u;
+                } else {
+                    spread(w.scale[f][s], scale[f]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u32x4 t[MF][P];
+#pragma unroll
+                for (int i = 0; i < MF; ++i) cut_unit<DT, P>(u[s][i][j], t[i]);
+#pragma unroll
+                for (int f = 0; f < NF; ++f) {
+                    const u32x4 v = decode8(codes[f][j], __uint_as_float(scale[f][j] << 23));
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+#pragma unroll
+                        for (int i = 0; i < MF; ++i) acc[f][i] = mfma<false>(v, t[i][p], acc[f][i]);
+                }
+            }
+        }
+    };
+    if (!none) {
+        Span w;
+        for (uint32_t b = wave * 16; b < blocks; b += KW * 16) {
+            load_rows(b);
+            load_weights(w, b);
+            __builtin_amdgcn_sched_barrier(0);       // everything asked for before anything is waited for
+            products(w);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NF * MF; ++i) part[wave][i][lane] = acc[i / MF][i % MF];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NF * MF; i += KW) {
+        if (i + wave >= NF * MF) break;
+        const int k = i + wave;
+        f32x4 v = part[0][k][lane];
+#pragma unroll
+        for (int w = 1; w < KW; ++w) v += part[w][k][lane];
+        const int64_t r = row + k % MF * 16 + m, c = col + k / MF * 16 + 4 * q;
+        if (r < end && c < nn) store4(a.out, a.out_t, (size_t)r * nn + c, v);
+    }
+}
+
+template <int DT, int MF, int NF, int KW>
+hipError_t launch_thin(const Grouped& a, hipStream_t st)
+{
+    const size_t cols = (a.n + 16 * NF - 1) / (16 * NF), some = a.rows < (size_t)a.experts + 2 ? a.rows : (size_t)a.experts + 2;
+    const size_t tiles = a.rows / (16 * MF) + some;
+    if (tiles > kMaxGrid / cols) return hipErrorInvalidConfiguration;
+    const dim3 grid((unsigned)(tiles * cols)), group(64 * KW);
+    if (a.k % 512 == 0) hipLaunchKernelGGL((grouped_thin_kernel<DT, MF, NF, KW, true>), grid, group, 0, st, a, (unsigned)cols);
+    else hipLaunchKernelGGL((grouped_thin_kernel<DT, MF, NF, KW, false>), grid, group, 0, st, a, (unsigned)cols);
+    return hipGetLastError();
+}
+
+// ---- some rows per expert -----------------------------------------------
+//
+// As above, but the waves of a workgroup share their rows: each of WN waves
+// forms 16 MF rows by 16 NF columns of its own over the whole contraction, the
+// weights straight to registers again, two spans of SB blocks in turn, and the
+// rows' spans pass through LDS, cut into terms once for all waves.
+
+// Byte offset of 16-byte unit c of row r in a span of SB blocks of 32.
+template <int SB>
+__device__ __forceinline__ uint32_t span_at(uint32_t r, uint32_t c) { return r * (SB * 64) + ((c ^ (r & 15)) << 4); }
+
+template <int DT, int MF, int NF, int WN, int SB, bool SPANS>
+__global__ __launch_bounds__(64 * WN) void grouped_slim_kernel(const Grouped a, unsigned cols)
+{
+    constexpr int P = Terms<DT>::v, ES = Elem<DT>::size, RU = DT == kF32 ? 2 : 1, S = SB / 4, T = 64 * WN;
+    constexpr uint32_t kOut = 0xFFFFFF00u, PLANE = 16 * MF * SB * 64, BUF = P * PLANE;
+    constexpr int UX = 16 * MF * SB * 4 / T;         // 16-byte units of a lane
+    static_assert(UX * T == 16 * MF * SB * 4, "units and threads");
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), m = lane & 15, q = lane >> 4;
+    const int64_t nn = a.n, kk = a.k, col = (int64_t)(blockIdx.x % cols) * (16 * NF * WN) + wave * (16 * NF);
+    const uint32_t blocks = (uint32_t)(kk / 32);
+    int seg;
+    int64_t row, end;
+    if (!find_tile<16 * MF>(a.offsets, a.experts, a.rows, blockIdx.x / cols, seg, row, end)) return;
+    const bool none = seg == 0 || seg > a.experts;   // rows of no expert: zeros
+    const bool live = col < nn && !none;             // a wave past the last column loads nothing
+    const int64_t fb = ((int64_t)(seg - 1) * nn + col) * blocks;
+    const uint32_t wrows = live ? (uint32_t)(nn - col < 16 * NF ? nn - col : 16 * NF) : 0, skip = (uint32_t)(fb & 63);
+    const uint32_t xrows = (uint32_t)(end - row < 16 * MF ? end - row : 16 * MF);
+    const Rsrc wr = span_rsrc(a.w, live ? (size_t)(fb >> 6) * 1088 : 0, live ? (skip + wrows * blocks + 63) / 64 * 1088 : 0);
+    const Rsrc xr = span_rsrc(a.a, (size_t)row * kk * ES, xrows * (uint32_t)kk * ES);
+    uint32_t first[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) first[f] = 16 * f + m < wrows ? skip + (16 * f + m) * blocks : kOut;
+    f32x4 acc[NF][MF];
+#pragma unroll
+    for (int i = 0; i < NF * MF; ++i) acc[i / MF][i % MF] = f32x4{0, 0, 0, 0};
+
+    struct Span { u32x4 codes[NF][S]; uint32_t scale[NF][S]; };
+    auto load_weights = [&](Span& w, uint32_t b0) {
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+            if constexpr (SPANS) {
+                const uint32_t at = first[f] + b0;
+                const uint32_t tile = (first[f] == kOut || b0 >= blocks) ? kOut : (at >> 6) * 1088, in = at & 63;
+                if constexpr (S == 4) {
+                    const u32x4 sc = __builtin_amdgcn_raw_buffer_load_b128(wr, tile == kOut ? kOut : tile + 1024 + in, 0, 0);
+#pragma unroll
+                    for (int s = 0; s < S; ++s) w.scale[f][s] = sc[s];
+                } else if constexpr (S == 1) {
+                    w.scale[f][0] = __builtin_amdgcn_raw_buffer_load_b32(wr, tile == kOut ? kOut : tile + 1024 + in, 0, 0);
+                } else {
+                    const u32x2 sc = __builtin_amdgcn_raw_buffer_load_b64(wr, tile == kOut ? kOut : tile + 1024 + in, 0, 0);
+#pragma unroll
+                    for (int s = 0; s < S; ++s) w.scale[f][s] = sc[s];
+                }
+#pragma unroll
+                for (int s = 0; s < S; ++s)
+                    w.codes[f][s] = __builtin_amdgcn_raw_buffer_load_b128(wr, tile == kOut ? kOut : tile + (in + q + 4 * s) * 16, 0, 0);
+            } else {
+#pragma unroll
+                for (int s = 0; s < S; ++s) {
+                    const uint32_t b = b0 + q + 4 * s, at = first[f] + b;
+                    const bool in = first[f] != kOut && b < blocks;
+                    w.codes[f][s] = __builtin_amdgcn_raw_buffer_load_b128(wr, in ? (at >> 6) * 1088 + (at & 63) * 16 : kOut, 0, 0);
+                    w.scale[f][s] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(wr, in ? (at >> 6) * 1088 + 1024 + (at & 63) : kOut, 0, 0);
+                }
+            }
+        }
+    };
+    Unit<DT> u[UX];
+    auto load_rows = [&](uint32_t b0) {              // this lane's units of the rows' span, to registers
+#pragma unroll
+        for (int i = 0; i < UX; ++i) {
+            const uint32_t s = i * T + tid, r = s / (SB * 4), c = s % (SB * 4);
+            const uint32_t off = (r < xrows && b0 + c / 4 < blocks) ? (r * (uint32_t)kk + b0 * 32 + c * 8) * ES : kOut;
+#pragma unroll
+            for (int h = 0; h < RU; ++h) u[i].v[h] = __builtin_amdgcn_raw_buffer_load_b128(xr, off + 16 * h, 0, 0);
+        }
+    };
+    auto store_rows = [&](uint8_t* buf) {            // and from there, as terms, to LDS
+#pragma unroll
+        for (int i = 0; i < UX; ++i) {
+            const uint32_t s = i * T + tid;
+            u32x4 t[P];
+            cut_unit<DT, P>(u[i], t);
+#pragma unroll
+            for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4*>(buf + p * PLANE + span_at<SB>(s / (SB * 4), s % (SB * 4))) = t[p];
+        }
+    };
+    auto products = [&](const Span& w, const uint8_t* buf) {
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            u32x4 codes[NF];
+            uint32_t scale[NF][4];
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                codes[f] = exchange(w.codes[f][s]);
+                if constexpr (SPANS) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) scale[f][j] = w.scale[f][s] >> (8 * j) & 255u;
+                } else {
+                    spread(w.scale[f][s], scale[f]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                u32x4 t[MF][P];
+#pragma unroll
+                for (int i = 0; i < MF; ++i)
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+                        t[i][p] = *reinterpret_cast<const u32x4*>(buf + p * PLANE + span_at<SB>(16 * i + m, 16 * s + 4 * j + q));
+#pragma unroll
+                for (int f = 0; f < NF; ++f) {
+                    const u32x4 v = decode8(codes[f][j], __uint_as_float(scale[f][j] << 23));
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+#pragma unroll
+                        for (int i = 0; i < MF; ++i) acc[f][i] = mfma<false>(v, t[i][p], acc[f][i]);
+                }
+            }
+        }
+    };
+    if (!none) {
+        // the rows' next span is asked for before the next weights, so it can be stored while those are in flight
+        Span w0, w1;
+        load_rows(0);
+        load_weights(w0, 0);
+        store_rows(lds);
+        __syncthreads();
+        for (uint32_t b = 0; b < blocks; b += 2 * SB) {
+            load_rows(b + SB);
+            load_weights(w1, b + SB);
+            __builtin_amdgcn_sched_barrier(0);
+            products(w0, lds);
+            store_rows(lds + BUF);
+            __syncthreads();
+            load_rows(b + 2 * SB);
+            load_weights(w0, b + 2 * SB);
+            __builtin_amdgcn_sched_barrier(0);
+            products(w1, lds + BUF);
+            store_rows(lds);
+            __syncthreads();
+        }
+    }
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+            const int64_t r = row + 16 * i + m, c = col + 16 * f + 4 * q;
+            if (r < end && c < nn) store4(a.out, a.out_t, (size_t)r * nn + c, acc[f][i]);
+        }
+}
+
+template <int DT, int MF, int NF, int WN, int SB>
+hipError_t launch_slim(const Grouped& a, hipStream_t st)
+{
+    constexpr size_t bytes = 2 * (size_t)Terms<DT>::v * 16 * MF * SB * 64;
+    static_assert(bytes <= 160 * 1024, "LDS");
+    const size_t cols = (a.n + 16 * NF * WN - 1) / (16 * NF * WN), some = a.rows < (size_t)a.experts + 2 ? a.rows : (size_t)a.experts + 2;
+    const size_t tiles = a.rows / (16 * MF) + some;
+    if (tiles > kMaxGrid / cols) return hipErrorInvalidConfiguration;
+    const auto kernel = a.k % (SB * 32) == 0 ? &grouped_slim_kernel<DT, MF, NF, WN, SB, true> : &grouped_slim_kernel<DT, MF, NF, WN, SB, false>;
+    if (bytes > 64 * 1024) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * cols)), dim3(64 * WN), bytes, st, a, (unsigned)cols);
+    return hipGetLastError();
+}
+
+template <int DIR, int DT, int BM, int BN, int WM, int WN, int BK = 64>
 hipError_t launch_tile(const Grouped& a, hipStream_t st)
 {
-    constexpr size_t bytes = 2 * (size_t)(Planes<DIR, DT>::a * BM + Planes<DIR, DT>::b * BN) * kBK * 2;
+    constexpr size_t bytes = 2 * (size_t)(Planes<DIR, DT>::a * BM + Planes<DIR, DT>::b * BN) * BK * 2;
     static_assert(bytes <= 160 * 1024, "LDS");
-    const size_t cols = ((DIR == kFwd ? a.n : a.k) + BN - 1) / BN;
+    const size_t cols = (a.k + BN - 1) / BN;
     const size_t some = a.rows < (size_t)a.experts + 2 ? a.rows : (size_t)a.experts + 2;   // segments that end inside a tile
     const size_t tiles = DIR == kDw ? (size_t)((a.n + BM - 1) / BM) * a.experts : a.rows / BM + some;
     if (tiles > kMaxGrid / cols) return hipErrorInvalidConfiguration;
-    const auto kernel = &grouped_tile_kernel<DIR, DT, BM, BN, WM, WN>;
+    const auto kernel = &grouped_tile_kernel<DIR, DT, BM, BN, WM, WN, BK>;
     if (bytes > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
@@ -398,25 +722,72 @@ hipError_t launch_tile(const Grouped& a, hipStream_t st)
     return hipGetLastError();
 }
 
-template <int DIR, int DT>
-hipError_t launch_t(const Grouped& a, hipStream_t st)
+// Forward.  The mean rows of an expert choose how many rows a workgroup takes
+// (the weights are read and decoded once per 16 MF rows, but rows that are not
+// there cost as much as others).  bf16, 32 experts of 2048 x 4096, in us with
+// 16, 32, 64, 128 rows: mean 6: 39, 39, 45, -; mean 16: 51, 51, 55, -; mean 64:
+// 114, 87, 83, 105; mean 128: -, -, 124, 136; mean 256: -, -, 208, 196.  Twice
+// the columns pay once there are tiles for several rounds of the card: 16384
+// rows of 8192 x 4096 1.16 ms -> 1.10, but 8192 rows of 2048 x 4096 180 us ->
+// 196.  Few workgroups of the shared form leave the card idle, and the
+// contraction is cut instead: two rows of 4096 x 4096 take 8 us so, 14 us
+// otherwise; 248 workgroups 9.4 and 8.2 us.
+template <int DT>
+hipError_t launch_forward(const Grouped& a, hipStream_t st)
 {
-    if constexpr (DT == kF32 && DIR == kDw) return launch_tile<DIR, DT, 128, 64, 2, 2>(a, st);
-    else if constexpr (DT == kF32) return launch_tile<DIR, DT, 128, 256, 2, 4>(a, st);
-    else if constexpr (DT == kF16 && DIR != kDw) return launch_tile<DIR, DT, 128, 256, 2, 4>(a, st);
-    else return launch_tile<DIR, DT, 256, 256, 2, 4>(a, st);
+    constexpr int SB = Terms<DT>::v == 1 ? 16 : 8;
+    const size_t mean = (a.rows + a.experts - 1) / a.experts;
+    const size_t groups = std::min(a.rows, a.rows / 16 + (size_t)a.experts) * ((a.n + 127) / 128);
+    if (groups < 192) return launch_thin<DT, 1, 2, 4>(a, st);
+    if (mean <= 8) return launch_slim<DT, 1, 1, 8, SB>(a, st);
+    if (mean <= 40) return launch_slim<DT, 2, 1, 8, SB>(a, st);
+    if constexpr (DT != kBF16) {
+        return launch_slim<DT, 4, 2, 8, 4>(a, st);
+    } else {
+        if (mean <= 160) return launch_slim<DT, 4, 1, 8, 8>(a, st);
+        if ((a.rows / 128 + a.experts) * ((a.n + 255) / 256) < 1024) return launch_slim<DT, 8, 1, 8, 4>(a, st);
+        return launch_slim<DT, 8, 2, 8, 4>(a, st);
+    }
+}
+
+// Gradients: small tiles until there are rows enough to fill large ones.  dx,
+// 16 experts of 2048 x 4096 in bf16, in us with 64 x 128, 128 x 128, 256 x 256:
+// mean 8: 32, 41, 67; mean 64: 43, 58, 69; mean 512: 221, 207, 215; mean 2048:
+// 799, 684, 639.  dW, 128 x 128 and 256 x 256: mean 8: 105, 128; mean 64: 136,
+// 136; mean 512: 297, 262.
+template <int DIR, int DT>
+hipError_t launch_backward(const Grouped& a, hipStream_t st)
+{
+    const size_t mean = (a.rows + a.experts - 1) / a.experts;
+    if constexpr (DIR == kDx && DT == kBF16) {
+        if (mean <= 128) return launch_tile<DIR, DT, 64, 128, 2, 2>(a, st);
+        if (mean <= 768) return launch_tile<DIR, DT, 128, 128, 2, 2>(a, st);
+        return launch_tile<DIR, DT, 256, 256, 2, 4>(a, st);
+    } else if constexpr (DIR == kDx) {
+        if (mean <= 128) return launch_tile<DIR, DT, 64, 128, 2, 2>(a, st);
+        return launch_tile<DIR, DT, 128, 256, 2, 4>(a, st);
+    } else if constexpr (DT == kF32) {
+        return launch_tile<DIR, DT, 128, 128, 2, 4, 32>(a, st);
+    } else {
+        if (mean <= 64) return launch_tile<DIR, DT, 128, 128, 2, 2>(a, st);
+        return launch_tile<DIR, DT, 256, 256, 2, 4>(a, st);
+    }
 }
 
 template <int DIR>
-hipError_t launch_dir(int dt, const Grouped& a, hipStream_t st)
+hipError_t launch_backward_rt(int dt, const Grouped& a, hipStream_t st)
 {
-    return dt == kF32 ? launch_t<DIR, kF32>(a, st) : dt == kF16 ? launch_t<DIR, kF16>(a, st) : launch_t<DIR, kBF16>(a, st);
+    return dt == kF32 ? launch_backward<DIR, kF32>(a, st) : dt == kF16 ? launch_backward<DIR, kF16>(a, st) : launch_backward<DIR, kBF16>(a, st);
 }
 
 }  // namespace
 
-hipError_t launch_grouped_forward(int dt, const Grouped& a, hipStream_t st) { return launch_dir<kFwd>(dt, a, st); }
-hipError_t launch_grouped_dx(int dt, const Grouped& a, hipStream_t st) { return launch_dir<kDx>(dt, a, st); }
-hipError_t launch_grouped_dw(int dt, const Grouped& a, hipStream_t st) { return launch_dir<kDw>(dt, a, st); }
+hipError_t launch_grouped_forward(int dt, const Grouped& a, hipStream_t st)
+{
+    return dt == kF32 ? launch_forward<kF32>(a, st) : dt == kF16 ? launch_forward<kF16>(a, st) : launch_forward<kBF16>(a, st);
+}
+
+hipError_t launch_grouped_dx(int dt, const Grouped& a, hipStream_t st) { return launch_backward_rt<kDx>(dt, a, st); }
+hipError_t launch_grouped_dw(int dt, const Grouped& a, hipStream_t st) { return launch_backward_rt<kDw>(dt, a, st); }
 
 }  // namespace rc
