@@ -25,6 +25,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 import os
 
 import torch  # must load before librcodec.so: both share torch's HIP runtime
@@ -35,6 +36,7 @@ LIB_PATH = os.path.join(_HERE, "librcodec.so")
 TILE = 2048
 BLOCK = 32
 MAX_STREAMS = 16
+MXFP4_TILE_BYTES = 1088
 
 FMT_INT4, FMT_INT3, FMT_FP8_E4M3, FMT_MXFP4, FMT_FP8_E5M2 = 1, 2, 3, 4, 5
 SCALE_FP16, SCALE_FP32, SCALE_E8M0 = 1, 2, 3
@@ -167,7 +169,7 @@ def _mine(t: torch.Tensor, stream) -> torch.Tensor:
 
 
 def _check_dev(t: torch.Tensor, name: str):
-    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -372,6 +374,18 @@ def _result(out, shape, dtype, like: torch.Tensor, stream, name: str) -> torch.T
     return out
 
 
+def _launch(what: str, dev: torch.device, stream, *args):
+    """The library's function on the device and stream; its status checked."""
+    hs = _stream(stream, dev)
+    if dev.index == torch.cuda.current_device():
+        status = getattr(_lib or lib(), what)(*args, hs)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(_lib or lib(), what)(*args, hs)
+    if status != OK:
+        raise CodecError(status, what)
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -390,7 +404,8 @@ def _rows_of(t: torch.Tensor, name: str, offsets: torch.Tensor):
 def _weights(w_packed: torch.Tensor, experts: int, n: int, k: int, dev):
     _check_dev(w_packed, "w_packed")
     _same_device(dev, ("w_packed", w_packed))
-    if n < 0 or k < 0 or w_packed.dtype != torch.uint8 or w_packed.numel() < packed_bytes(MXFP4, experts * n * k):
+    tiles = -(-experts * n * k // TILE)
+    if n < 0 or k < 0 or w_packed.dtype != torch.uint8 or w_packed.numel() < tiles * MXFP4_TILE_BYTES:
         raise ValueError("w_packed must hold packed_bytes(MXFP4, experts * n * k) bytes")
 
 
@@ -404,13 +419,11 @@ def mxfp4_grouped_matmul(x: torch.Tensor, w_packed: torch.Tensor, offsets: torch
     rc_mxfp4_grouped_matmul."""
     rows, k, experts = _rows_of(x, "x", offsets)
     _weights(w_packed, experts, n, k, x.device)
-    hs = _stream(stream, x.device)
     y_t = x.dtype if out_dtype is None else out_dtype
     xt, yt = _dtype(x.dtype, "x"), _dtype(y_t, "output")
     out = _result(out, (rows, n), y_t, x, stream, "out")
-    with torch.cuda.device(x.device):
-        _ok(lib().rc_mxfp4_grouped_matmul(w_packed.data_ptr(), experts, n, k, offsets.data_ptr(), xt, x.data_ptr(),
-                                          rows, yt, out.data_ptr(), hs), "rc_mxfp4_grouped_matmul")
+    _launch("rc_mxfp4_grouped_matmul", x.device, stream, w_packed.data_ptr(), experts, n, k, offsets.data_ptr(), xt,
+            x.data_ptr(), rows, yt, out.data_ptr())
     return out
 
 
@@ -421,14 +434,11 @@ def mxfp4_grouped_matmul_dx(dy: torch.Tensor, w_packed: torch.Tensor, offsets: t
     dy (rows x n); rows x k of out_dtype (dy's by default)."""
     rows, n, experts = _rows_of(dy, "dy", offsets)
     _weights(w_packed, experts, n, k, dy.device)
-    hs = _stream(stream, dy.device)
     dx_t = dy.dtype if out_dtype is None else out_dtype
     yt, xt = _dtype(dy.dtype, "dy"), _dtype(dx_t, "output")
     out = _result(out, (rows, k), dx_t, dy, stream, "out")
-    with torch.cuda.device(dy.device):
-        _ok(lib().rc_mxfp4_grouped_matmul_dx(w_packed.data_ptr(), experts, n, k, offsets.data_ptr(), yt,
-                                             dy.data_ptr(), rows, xt, out.data_ptr(), hs),
-            "rc_mxfp4_grouped_matmul_dx")
+    _launch("rc_mxfp4_grouped_matmul_dx", dy.device, stream, w_packed.data_ptr(), experts, n, k, offsets.data_ptr(),
+            yt, dy.data_ptr(), rows, xt, out.data_ptr())
     return out
 
 
@@ -443,12 +453,10 @@ def grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
     if x.dim() != 2 or x.shape[0] != rows or x.dtype != dy.dtype:
         raise ValueError("x must have dy's rows and dtype")
     k = x.shape[1]
-    hs = _stream(stream, dy.device)
     t, wt = _dtype(dy.dtype, "dy"), _dtype(out_dtype, "output")
     out = _result(out, (experts, n, k), out_dtype, dy, stream, "out")
-    with torch.cuda.device(dy.device):
-        _ok(lib().rc_grouped_matmul_dw(experts, n, k, offsets.data_ptr(), t, dy.data_ptr(), x.data_ptr(), rows, wt,
-                                       out.data_ptr(), hs), "rc_grouped_matmul_dw")
+    _launch("rc_grouped_matmul_dw", dy.device, stream, experts, n, k, offsets.data_ptr(), t, dy.data_ptr(),
+            x.data_ptr(), rows, wt, out.data_ptr())
     return out
 
 
@@ -501,14 +509,11 @@ def block_norm(y: torch.Tensor, residual: torch.Tensor, pre_weight: torch.Tensor
     _like(residual, y, "residual")
     wt, mode = _norm_weights(y, d, pre_weight, post_weight, gate)
     t = _dtype(y.dtype, "y")
-    hs = _stream(stream, y.device)
     h = _result(h, y.shape, y.dtype, y, stream, "h")
     z = _result(z, y.shape, y.dtype, y, stream, "z")
     st = _result(None, (2, rows), torch.float32, y, stream, "stats") if stats else None
-    with torch.cuda.device(y.device):
-        _ok(lib().rc_block_norm(t, rows, d, y.data_ptr(), residual.data_ptr(), wt, _ptr(post_weight), mode,
-                                _ptr(gate), pre_weight.data_ptr(), residual_scale, eps, h.data_ptr(), z.data_ptr(),
-                                _ptr(st), hs), "rc_block_norm")
+    _launch("rc_block_norm", y.device, stream, t, rows, d, y.data_ptr(), residual.data_ptr(), wt, _ptr(post_weight),
+            mode, _ptr(gate), pre_weight.data_ptr(), residual_scale, eps, h.data_ptr(), z.data_ptr(), _ptr(st))
     return h, z, st
 
 
@@ -534,7 +539,6 @@ def block_norm_backward(dz: torch.Tensor, dh: torch.Tensor | None, h: torch.Tens
         raise ValueError("stats must hold 2 x rows float32 values")
     wt, mode = _norm_weights(y, d, pre_weight, post_weight, gate)
     t = _dtype(y.dtype, "y")
-    hs = _stream(stream, y.device)
     dy = _result(dy, y.shape, y.dtype, y, stream, "dy")
     dr = _result(dresidual, y.shape, y.dtype, y, stream, "dresidual")
     new = lambda shape, dt: _mine(torch.empty(shape, dtype=dt, device=y.device), stream)  # noqa: E731
@@ -542,13 +546,30 @@ def block_norm_backward(dz: torch.Tensor, dh: torch.Tensor | None, h: torch.Tens
     dpost = new((d,), torch.float32) if post_weight is not None else None
     dgate = None if gate is None else new((d,), torch.float32) if mode == GATE_CHANNEL else new(y.shape, y.dtype)
     ws = new((lib().rc_block_norm_backward_workspace(rows, d),), torch.uint8)
-    with torch.cuda.device(y.device):
-        _ok(lib().rc_block_norm_backward(t, rows, d, dz.data_ptr(), _ptr(dh), h.data_ptr(), stats.data_ptr(),
-                                         y.data_ptr(), wt, _ptr(post_weight), mode, _ptr(gate),
-                                         pre_weight.data_ptr(), residual_scale, dy.data_ptr(), dr.data_ptr(),
-                                         dpre.data_ptr(), _ptr(dpost), _ptr(dgate), ws.data_ptr(), hs),
-            "rc_block_norm_backward")
+    _launch("rc_block_norm_backward", y.device, stream, t, rows, d, dz.data_ptr(), _ptr(dh), h.data_ptr(),
+            stats.data_ptr(), y.data_ptr(), wt, _ptr(post_weight), mode, _ptr(gate), pre_weight.data_ptr(),
+            residual_scale, dy.data_ptr(), dr.data_ptr(), dpre.data_ptr(), _ptr(dpost), _ptr(dgate), ws.data_ptr())
     return dy, dr, dpre, dpost, dgate
+
+
+_dtype_of = operator.attrgetter("dtype")
+
+
+def _tensors(tensors, dev: torch.device, name: str):
+    """(addresses, sizes, type codes) of contiguous tensors on `dev`; a few
+    hundred of them are looked at per call, hence the maps over C methods."""
+    T = torch.Tensor
+    try:
+        if set(map(T.get_device, tensors)) == {dev.index} and all(map(T.is_contiguous, tensors)):
+            return (array.array("Q", map(T.data_ptr, tensors)), array.array("Q", map(T.numel, tensors)),
+                    memoryview(array.array("I", map(_DTYPES.__getitem__, map(_dtype_of, tensors)))))
+    except (TypeError, KeyError):
+        pass
+    for j, t in enumerate(tensors):                          # something is refused: say which
+        _check_dev(t, f"{name}[{j}]")
+        _same_device(dev, (f"{name}[{j}]", t))
+        _dtype(t.dtype, f"{name}[{j}]")
+    raise ValueError(f"{name} must hold GPU tensors")
 
 
 def grad_norm_clip(grads, max_norm: float, scale: float = 1.0, eps: float = 1e-6, out=None,
@@ -564,26 +585,26 @@ def grad_norm_clip(grads, max_norm: float, scale: float = 1.0, eps: float = 1e-6
         raise ValueError("need at least one tensor")
     if len(outs) != len(grads):
         raise ValueError("out must hold one tensor for each of grads")
+    _check_dev(grads[0], "grads[0]")
     dev = grads[0].device
-    desc = array.array("Q")
-    for j, (g, o) in enumerate(zip(grads, outs)):
-        _check_dev(g, f"grads[{j}]")
-        if o is not g:
-            _check_dev(o, f"out[{j}]")
-            if o.numel() != g.numel():
-                raise ValueError(f"out[{j}] must hold as many values as grads[{j}]")
-        _same_device(dev, (f"grads[{j}]", g), (f"out[{j}]", o))
-        desc.extend((g.data_ptr(), o.data_ptr(), g.numel(),
-                     _dtype(g.dtype, "gradient") | _dtype(o.dtype, "output") << 32))
-    hs = _stream(stream, dev)
+    desc = array.array("Q", bytes(32 * len(grads)))          # rc_grad: in, out, n, and in_t, out_t as halves
+    ptrs, numels, types = _tensors(grads, dev, "grads")
+    desc[0::4], desc[2::4] = ptrs, numels
+    if outs is grads:
+        desc[1::4], out_types = ptrs, types
+    else:
+        desc[1::4], out_numels, out_types = _tensors(outs, dev, "out")
+        if out_numels != numels:
+            raise ValueError("each tensor of out must hold as many values as its gradient")
+    halves = memoryview(desc).cast("B").cast("I")
+    halves[6::8], halves[7::8] = types, out_types
     if norm is None:
         norm = _mine(torch.empty(1, dtype=torch.float32, device=dev), stream)
     _check_dev(norm, "norm")
     _same_device(dev, ("norm", norm))
     if norm.dtype != torch.float32 or norm.numel() < 1:
         raise ValueError("norm must hold one float32 value")
-    ws = _mine(torch.empty(lib().rc_grad_norm_clip_workspace(), dtype=torch.uint8, device=dev), stream)
-    with torch.cuda.device(dev):
-        _ok(lib().rc_grad_norm_clip(desc.buffer_info()[0], len(grads), scale, max_norm, eps, ws.data_ptr(),
-                                    norm.data_ptr(), hs), "rc_grad_norm_clip")
+    ws = _mine(torch.empty((_lib or lib()).rc_grad_norm_clip_workspace(), dtype=torch.uint8, device=dev), stream)
+    _launch("rc_grad_norm_clip", dev, stream, desc.buffer_info()[0], len(grads), scale, max_norm, eps, ws.data_ptr(),
+            norm.data_ptr())
     return norm

@@ -20,17 +20,51 @@
 namespace rc {
 namespace {
 
-// The weights of a lane's N vectors of E elements, T lanes apart.
+// E neighbouring weights from element i (a multiple of E) on, of type WT.
+template <int WT, int E>
+__device__ __forceinline__ void weights_at(const void* w, uint32_t i, uint32_t d, float* v)
+{
+    const uint8_t* p = static_cast<const uint8_t*>(w) + (size_t)i * Elem<WT>::size;
+    if (i + E <= d) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4) {
+            if constexpr (WT == kF32) {
+                const u32x4 u = reinterpret_cast<const u32x4*>(p)[e / 4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[e + k] = __uint_as_float(u[k]);
+            } else {
+                const uint2 u = reinterpret_cast<const uint2*>(p)[e / 4];
+                v[e] = WT == kBF16 ? bf16lo(u.x) : f16lo(u.x);
+                v[e + 1] = WT == kBF16 ? bf16hi(u.x) : f16hi(u.x);
+                v[e + 2] = WT == kBF16 ? bf16lo(u.y) : f16lo(u.y);
+                v[e + 3] = WT == kBF16 ? bf16hi(u.y) : f16hi(u.y);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = i + e < d ? load1<WT>(w, i + e) : 0.0f;
+    }
+}
+
+// The weights of a lane's N vectors of E elements, T lanes apart; without
+// weights, `otherwise`.
 template <int E, int N, int T>
 __device__ __forceinline__ void load_weights(const void* w, int dt, uint32_t d, float (&v)[N * E], float otherwise)
 {
 #pragma unroll
-    for (int j = 0; j < N; ++j)
+    for (int j = 0; j < N; ++j) {
+        const uint32_t i = (j * T + threadIdx.x) * E;
+        if (!w) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const uint32_t i = (j * T + threadIdx.x) * E + e;
-            v[j * E + e] = w ? (i < d ? load1_rt(w, dt, i) : 0.0f) : otherwise;
+            for (int e = 0; e < E; ++e) v[j * E + e] = otherwise;
+        } else if (dt == kF32) {
+            weights_at<kF32, E>(w, i, d, v + j * E);
+        } else if (dt == kBF16) {
+            weights_at<kBF16, E>(w, i, d, v + j * E);
+        } else {
+            weights_at<kF16, E>(w, i, d, v + j * E);
         }
+    }
 }
 
 template <int DT, int T, int N>
@@ -53,11 +87,9 @@ __global__ __launch_bounds__(T) void block_norm_kernel(const BlockNorm a)
     int turn = 0;
     for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         const size_t at = row * d * Elem<DT>::size;
-        const void* y = static_cast<const uint8_t*>(a.y) + at;
-        const void* r = static_cast<const uint8_t*>(a.r) + at;
         u32x4 uy[N], ur[N], ug[N];
-        load_row<DT>(y, i0, T * E, d, uy);
-        load_row<DT>(r, i0, T * E, d, ur);
+        load_row<DT>(static_cast<const uint8_t*>(a.y) + at, i0, T * E, d, uy);
+        load_row<DT>(static_cast<const uint8_t*>(a.r) + at, i0, T * E, d, ur);
         if (full) load_row<DT>(static_cast<const uint8_t*>(a.gate) + at, i0, T * E, d, ug);
         float rstd_y = 1.0f;
         if (post) {
@@ -115,14 +147,15 @@ __global__ __launch_bounds__(T) void block_norm_kernel(const BlockNorm a)
 // to one row of the workspace per workgroup, [2][d]: dz hn, and e yn (times a
 // full gate).  A channel gate and the post weight are the same for all rows,
 // so dw1 = g * sum(e yn) and dg = w1 * sum(e yn) come from one sum.
-template <int DT, int T, int N>
+template <int DT, int T, int N, bool FULL>
 __global__ __launch_bounds__(T) void block_norm_backward_kernel(const BlockNormBackward a)
 {
     constexpr int E = Elem<DT>::per16, W = T / 64, EN = E * N;
     __shared__ float slot[2][2][W];
     const uint32_t d = a.d, i0 = threadIdx.x * E;
     const float inv_d = 1.0f / (float)d;
-    const bool post = a.post_w != nullptr, full = a.gate_mode == kGateFull;
+    constexpr bool full = FULL;
+    const bool post = a.post_w != nullptr;
     float w1[EN], w2[EN], sum_pre[EN], sum_y[EN];
     load_weights<E, N, T>(a.post_w, a.w_t, d, w1, 1.0f);
     load_weights<E, N, T>(a.pre_w, a.w_t, d, w2, 1.0f);
@@ -135,15 +168,27 @@ __global__ __launch_bounds__(T) void block_norm_backward_kernel(const BlockNormB
 #pragma unroll
     for (int e = 0; e < EN; ++e) sum_pre[e] = sum_y[e] = 0.0f;
     int turn = 0;
+    u32x4 uy[N], uh[N], uz[N], ud[N], ug[N], pz[N], ph[N];
+    float rstd_y, rstd_h;
+    auto ask = [&](size_t row) {                 // the two that a row's first sum needs
+        const size_t at = row * d * Elem<DT>::size;
+        load_row<DT>(static_cast<const uint8_t*>(a.dz) + at, i0, T * E, d, pz);
+        load_row<DT>(static_cast<const uint8_t*>(a.h) + at, i0, T * E, d, ph);
+    };
+    // wide rows leave room for two workgroups per compute unit, too few to hide all loads: their next row's
+    // are in flight during this one (8192 x 4096 93 -> 90 us; narrow rows lose by it: 16384 x 1024 54 -> 55-61)
+    constexpr bool AHEAD = T >= 512;
+    if (AHEAD) ask(blockIdx.x);
     for (size_t row = blockIdx.x; row < a.rows; row += gridDim.x, turn ^= 1) {
         const size_t at = row * d * Elem<DT>::size;
-        u32x4 uy[N], uh[N], uz[N], ud[N], ug[N];
-        load_row<DT>(static_cast<const uint8_t*>(a.dz) + at, i0, T * E, d, uz);
-        load_row<DT>(static_cast<const uint8_t*>(a.h) + at, i0, T * E, d, uh);
+        if (!AHEAD) ask(row);
+#pragma unroll
+        for (int j = 0; j < N; ++j) { uz[j] = pz[j]; uh[j] = ph[j]; }
         if (a.dh) load_row<DT>(static_cast<const uint8_t*>(a.dh) + at, i0, T * E, d, ud);
         load_row<DT>(static_cast<const uint8_t*>(a.y) + at, i0, T * E, d, uy);
         if (full) load_row<DT>(static_cast<const uint8_t*>(a.gate) + at, i0, T * E, d, ug);
-        const float rstd_y = post ? a.stats[row] : 1.0f, rstd_h = a.stats[a.rows + row];
+        rstd_y = post ? a.stats[row] : 1.0f; rstd_h = a.stats[a.rows + row];
+        if (AHEAD && row + gridDim.x < a.rows) ask(row + gridDim.x);
         float s = 0.0f;
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -210,28 +255,40 @@ __global__ __launch_bounds__(T) void block_norm_backward_kernel(const BlockNormB
     }
 }
 
-// Adds the workgroups' column sums: 64 columns per workgroup, its four waves
-// take every fourth row of the workspace, then add up in order.
-__global__ __launch_bounds__(256) void block_norm_columns_kernel(const BlockNormBackward a, int parts)
+// Adds the workgroups' column sums: 64 of the workspace's 2 d columns per
+// workgroup, its 16 waves each a run of its rows (eight loads in flight), then
+// the waves' sums in order.  Columns d .. 2 d - 1 give dw1 and a channel
+// gate's gradient.
+__global__ __launch_bounds__(1024) void block_norm_columns_kernel(const BlockNormBackward a, int parts)
 {
-    __shared__ float half[2][4][64];
-    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = blockIdx.x * 64 + lane, d = a.d;
-    float p = 0.0f, s = 0.0f;
-    if (i < d) {
-#pragma unroll 4
-        for (int k = wave; k < parts; k += 4) {
-            p += a.partial[(size_t)k * 2 * d + i];
-            s += a.partial[(size_t)k * 2 * d + d + i];
+    __shared__ float sums[16][64];
+    const uint32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6, d = a.d, width = 2 * d;
+    const uint32_t c = blockIdx.x * 64 + lane, run = (parts + 15) / 16, first = wave * run, last = min(first + run, (uint32_t)parts);
+    float s = 0.0f;
+    if (c < width) {
+        const float* p = a.partial + (size_t)first * width + c;
+        uint32_t k = first;
+        for (; k + 8 <= last; k += 8, p += (size_t)8 * width) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = p[(size_t)i * width];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += v[i];
         }
+        for (; k < last; ++k, p += width) s += *p;
     }
-    half[0][wave][lane] = p;
-    half[1][wave][lane] = s;
+    sums[wave][lane] = s;
     __syncthreads();
-    if (wave != 0 || i >= d) return;
-    p = (half[0][0][lane] + half[0][1][lane]) + (half[0][2][lane] + half[0][3][lane]);
-    s = (half[1][0][lane] + half[1][1][lane]) + (half[1][2][lane] + half[1][3][lane]);
+    if (wave != 0 || c >= width) return;
+    s = sums[0][lane];
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += sums[w][lane];
+    if (c < d) {
+        a.dpre[c] = s;
+        return;
+    }
+    const uint32_t i = c - d;
     const bool channel = a.gate_mode == kGateChannel;
-    a.dpre[i] = p;
     if (a.dpost) a.dpost[i] = channel ? s * load1_rt(a.gate, a.w_t, i) : s;
     if (channel && a.dgate) static_cast<float*>(a.dgate)[i] = a.post_w ? s * load1_rt(a.post_w, a.w_t, i) : s;
 }
@@ -257,21 +314,24 @@ hipError_t with_shape(uint32_t d, F&& f)
 template <int DT>
 hipError_t forward_t(const BlockNorm& a, hipStream_t st)
 {
-    return with_shape<DT, 16>(a.d, [&](auto t, auto n) {
-        const size_t most = (size_t)compute_units() * (2048 / t);
+    const auto launch = [&](auto t, auto n) {
+        const size_t most = (size_t)compute_units() * ((t >= 512 ? 1024 : 2048) / t);
         hipLaunchKernelGGL((block_norm_kernel<DT, t, n>), dim3((unsigned)(a.rows < most ? a.rows : most)), dim3(t), 0, st, a);
         return hipGetLastError();
-    });
+    };
+    return a.d <= 4096 ? with_shape<DT, 8>(a.d, launch) : with_shape<DT, 16>(a.d, launch);
 }
 
 template <int DT>
 hipError_t backward_t(const BlockNormBackward& a, unsigned groups, hipStream_t st)
 {
-    return with_shape<DT, 8>(a.d, [&](auto t, auto n) {
-        if (groups) hipLaunchKernelGGL((block_norm_backward_kernel<DT, t, n>), dim3(groups), dim3(t), 0, st, a);
-        hipLaunchKernelGGL(block_norm_columns_kernel, dim3((a.d + 63) / 64), dim3(256), 0, st, a, (int)groups);
+    const auto launch = [&](auto t, auto n) {
+        if (groups && a.gate_mode == kGateFull) hipLaunchKernelGGL((block_norm_backward_kernel<DT, t, n, true>), dim3(groups), dim3(t), 0, st, a);
+        else if (groups) hipLaunchKernelGGL((block_norm_backward_kernel<DT, t, n, false>), dim3(groups), dim3(t), 0, st, a);
+        hipLaunchKernelGGL(block_norm_columns_kernel, dim3((2 * a.d + 63) / 64), dim3(1024), 0, st, a, (int)groups);
         return hipGetLastError();
-    });
+    };
+    return with_shape<DT, 8>(a.d, launch);
 }
 
 }  // namespace

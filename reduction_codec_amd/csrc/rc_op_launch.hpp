@@ -45,9 +45,19 @@ struct BlockNormBackward {
     int gate_mode, w_t;
     float alpha;
 };
-// Workgroups of the backward kernel (rows of its workspace): by sizes alone,
-// so the workspace can be sized without a GPU.  Two per compute unit of 256.
-inline unsigned block_norm_groups(size_t rows, uint32_t) { return (unsigned)(rows < 512 ? rows : 512); }
+// Workgroups of the backward kernel, rows of its workspace: by sizes alone, so
+// the workspace can be sized without a GPU.  T lanes of eight elements hold a
+// row; 1024 lanes per unit of 256 for wide rows, 512 for narrow ones, whose
+// many small workgroups fill the units less evenly (measured at 256 .. 2048
+// workgroups: d = 8192 161, 174, 198 us; 4096 100, 90, 100; 2048 71, 52, 62;
+// 1024 117, 71, 54, 66; every workgroup costs 8 d bytes written and read).
+inline unsigned block_norm_groups(size_t rows, uint32_t d)
+{
+    unsigned t = 64;
+    while (t < 1024 && t * 8 < d) t *= 2;
+    const unsigned most = t >= 512 ? 256 * 1024 / t : 256 * 512 / t;
+    return (unsigned)(rows < most ? rows : most);
+}
 hipError_t launch_block_norm(int dt, const BlockNorm& a, hipStream_t st);
 hipError_t launch_block_norm_backward(int dt, const BlockNormBackward& a, hipStream_t st);
 
