@@ -18,7 +18,7 @@ inline int compute_units()
 }
 
 // ---- gradient norm and clipping (rc_op_grad_clip.hip)
-constexpr unsigned kClipGroups = 2048;           // most workgroups of a launch, one partial sum each
+constexpr unsigned kClipGroups = 1024;           // most workgroups of a launch, one partial sum each
 struct GradTensor { const void* in; void* out; uint64_t n; int32_t in_t, out_t; };
 hipError_t launch_grad_norm_clip(const GradTensor* grads, size_t count, float scale, float max_norm, float eps,
                                  void* workspace, float* norm, hipStream_t st);
