@@ -363,12 +363,19 @@ def _dtype(dt: torch.dtype, name: str) -> int:
     return _DTYPES[dt]
 
 
-def _result(out, shape, dtype, like: torch.Tensor, stream, name: str) -> torch.Tensor:
+def _check_on(t: torch.Tensor, name: str, index: int):
+    """A contiguous tensor on GPU `index`."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or not t.is_contiguous():
+        _check_dev(t, name)
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _result(out, shape, dtype, dev: torch.device, stream, name: str) -> torch.Tensor:
     """The caller's output, checked, or a new one for work on `stream`."""
     if out is None:
-        return _mine(torch.empty(shape, dtype=dtype, device=like.device), stream)
-    _check_dev(out, name)
-    _same_device(like.device, (name, out))
+        out = torch.empty(shape, dtype=dtype, device=dev)
+        return out if stream is None else _mine(out, stream)
+    _check_on(out, name, dev.index)
     if out.dtype != dtype or tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
     return out
@@ -376,7 +383,7 @@ def _result(out, shape, dtype, like: torch.Tensor, stream, name: str) -> torch.T
 
 def _launch(what: str, dev: torch.device, stream, *args):
     """The library's function on the device and stream; its status checked."""
-    hs = _stream(stream, dev)
+    hs = torch.cuda.current_stream(dev.index).cuda_stream if stream is None else _stream(stream, dev)
     if dev.index == torch.cuda.current_device():
         status = getattr(_lib or lib(), what)(*args, hs)
     else:
@@ -392,8 +399,7 @@ def _ptr(t):
 
 def _rows_of(t: torch.Tensor, name: str, offsets: torch.Tensor):
     _check_dev(t, name)
-    _check_dev(offsets, "offsets")
-    _same_device(t.device, ("offsets", offsets))
+    _check_on(offsets, "offsets", t.get_device())
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, rows and width")
     if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2:
@@ -402,8 +408,7 @@ def _rows_of(t: torch.Tensor, name: str, offsets: torch.Tensor):
 
 
 def _weights(w_packed: torch.Tensor, experts: int, n: int, k: int, dev):
-    _check_dev(w_packed, "w_packed")
-    _same_device(dev, ("w_packed", w_packed))
+    _check_on(w_packed, "w_packed", dev.index)
     tiles = -(-experts * n * k // TILE)
     if n < 0 or k < 0 or w_packed.dtype != torch.uint8 or w_packed.numel() < tiles * MXFP4_TILE_BYTES:
         raise ValueError("w_packed must hold packed_bytes(MXFP4, experts * n * k) bytes")
@@ -418,11 +423,12 @@ def mxfp4_grouped_matmul(x: torch.Tensor, w_packed: torch.Tensor, offsets: torch
     Returns rows x n of out_dtype (x's by default).  See
     rc_mxfp4_grouped_matmul."""
     rows, k, experts = _rows_of(x, "x", offsets)
-    _weights(w_packed, experts, n, k, x.device)
+    dev = x.device
+    _weights(w_packed, experts, n, k, dev)
     y_t = x.dtype if out_dtype is None else out_dtype
     xt, yt = _dtype(x.dtype, "x"), _dtype(y_t, "output")
-    out = _result(out, (rows, n), y_t, x, stream, "out")
-    _launch("rc_mxfp4_grouped_matmul", x.device, stream, w_packed.data_ptr(), experts, n, k, offsets.data_ptr(), xt,
+    out = _result(out, (rows, n), y_t, dev, stream, "out")
+    _launch("rc_mxfp4_grouped_matmul", dev, stream, w_packed.data_ptr(), experts, n, k, offsets.data_ptr(), xt,
             x.data_ptr(), rows, yt, out.data_ptr())
     return out
 
@@ -433,11 +439,12 @@ def mxfp4_grouped_matmul_dx(dy: torch.Tensor, w_packed: torch.Tensor, offsets: t
     """dx[i] = W_e^T dy[i]: the gradient of mxfp4_grouped_matmul's rows, from
     dy (rows x n); rows x k of out_dtype (dy's by default)."""
     rows, n, experts = _rows_of(dy, "dy", offsets)
-    _weights(w_packed, experts, n, k, dy.device)
+    dev = dy.device
+    _weights(w_packed, experts, n, k, dev)
     dx_t = dy.dtype if out_dtype is None else out_dtype
     yt, xt = _dtype(dy.dtype, "dy"), _dtype(dx_t, "output")
-    out = _result(out, (rows, k), dx_t, dy, stream, "out")
-    _launch("rc_mxfp4_grouped_matmul_dx", dy.device, stream, w_packed.data_ptr(), experts, n, k, offsets.data_ptr(),
+    out = _result(out, (rows, k), dx_t, dev, stream, "out")
+    _launch("rc_mxfp4_grouped_matmul_dx", dev, stream, w_packed.data_ptr(), experts, n, k, offsets.data_ptr(),
             yt, dy.data_ptr(), rows, xt, out.data_ptr())
     return out
 
@@ -448,14 +455,14 @@ def grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
     """dW[e] = sum over expert e's rows of dy[i] x[i]^T (experts x n x k): the
     dense gradient of the weights before their cast to MXFP4."""
     rows, n, experts = _rows_of(dy, "dy", offsets)
-    _check_dev(x, "x")
-    _same_device(dy.device, ("x", x))
+    dev = dy.device
+    _check_on(x, "x", dev.index)
     if x.dim() != 2 or x.shape[0] != rows or x.dtype != dy.dtype:
         raise ValueError("x must have dy's rows and dtype")
     k = x.shape[1]
     t, wt = _dtype(dy.dtype, "dy"), _dtype(out_dtype, "output")
-    out = _result(out, (experts, n, k), out_dtype, dy, stream, "out")
-    _launch("rc_grouped_matmul_dw", dy.device, stream, experts, n, k, offsets.data_ptr(), t, dy.data_ptr(),
+    out = _result(out, (experts, n, k), out_dtype, dev, stream, "out")
+    _launch("rc_grouped_matmul_dw", dev, stream, experts, n, k, offsets.data_ptr(), t, dy.data_ptr(),
             x.data_ptr(), rows, wt, out.data_ptr())
     return out
 
@@ -463,10 +470,12 @@ def grouped_matmul_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
 def _norm_weights(like: torch.Tensor, d: int, pre_weight, post_weight, gate):
     """(weight type, gate mode) of a block norm; the gate is None, d values of
     the weights' type, or one per element of `like`, of its type."""
-    for name, w in (("pre_weight", pre_weight), ("post_weight", post_weight), ("gate", gate)):
-        if w is not None:
-            _check_dev(w, name)
-            _same_device(like.device, (name, w))
+    index = like.get_device()
+    _check_on(pre_weight, "pre_weight", index)
+    if post_weight is not None:
+        _check_on(post_weight, "post_weight", index)
+    if gate is not None:
+        _check_on(gate, "gate", index)
     wt = _dtype(pre_weight.dtype, "weight")
     if pre_weight.numel() != d or (post_weight is not None and
                                    (post_weight.numel() != d or post_weight.dtype != pre_weight.dtype)):
@@ -481,8 +490,7 @@ def _norm_weights(like: torch.Tensor, d: int, pre_weight, post_weight, gate):
 
 
 def _like(t: torch.Tensor, like: torch.Tensor, name: str):
-    _check_dev(t, name)
-    _same_device(like.device, (name, t))
+    _check_on(t, name, like.get_device())
     if t.shape != like.shape or t.dtype != like.dtype:
         raise ValueError(f"{name} must have y's shape and dtype")
 
@@ -509,10 +517,11 @@ def block_norm(y: torch.Tensor, residual: torch.Tensor, pre_weight: torch.Tensor
     _like(residual, y, "residual")
     wt, mode = _norm_weights(y, d, pre_weight, post_weight, gate)
     t = _dtype(y.dtype, "y")
-    h = _result(h, y.shape, y.dtype, y, stream, "h")
-    z = _result(z, y.shape, y.dtype, y, stream, "z")
-    st = _result(None, (2, rows), torch.float32, y, stream, "stats") if stats else None
-    _launch("rc_block_norm", y.device, stream, t, rows, d, y.data_ptr(), residual.data_ptr(), wt, _ptr(post_weight),
+    dev, shape, dtype = y.device, y.shape, y.dtype
+    h = _result(h, shape, dtype, dev, stream, "h")
+    z = _result(z, shape, dtype, dev, stream, "z")
+    st = _result(None, (2, rows), torch.float32, dev, stream, "stats") if stats else None
+    _launch("rc_block_norm", dev, stream, t, rows, d, y.data_ptr(), residual.data_ptr(), wt, _ptr(post_weight),
             mode, _ptr(gate), pre_weight.data_ptr(), residual_scale, eps, h.data_ptr(), z.data_ptr(), _ptr(st))
     return h, z, st
 
@@ -533,20 +542,20 @@ def block_norm_backward(dz: torch.Tensor, dh: torch.Tensor | None, h: torch.Tens
     rows = y.numel() // d
     for name, g in (("dz", dz), ("h", h)) + ((("dh", dh),) if dh is not None else ()):
         _like(g, y, name)
-    _check_dev(stats, "stats")
-    _same_device(y.device, ("stats", stats))
+    dev = y.device
+    _check_on(stats, "stats", dev.index)
     if stats.dtype != torch.float32 or stats.numel() != 2 * rows:
         raise ValueError("stats must hold 2 x rows float32 values")
     wt, mode = _norm_weights(y, d, pre_weight, post_weight, gate)
     t = _dtype(y.dtype, "y")
-    dy = _result(dy, y.shape, y.dtype, y, stream, "dy")
-    dr = _result(dresidual, y.shape, y.dtype, y, stream, "dresidual")
-    new = lambda shape, dt: _mine(torch.empty(shape, dtype=dt, device=y.device), stream)  # noqa: E731
+    dy = _result(dy, y.shape, y.dtype, dev, stream, "dy")
+    dr = _result(dresidual, y.shape, y.dtype, dev, stream, "dresidual")
+    new = lambda shape, dt: _result(None, shape, dt, dev, stream, "")  # noqa: E731
     dpre = new((d,), torch.float32)
     dpost = new((d,), torch.float32) if post_weight is not None else None
     dgate = None if gate is None else new((d,), torch.float32) if mode == GATE_CHANNEL else new(y.shape, y.dtype)
     ws = new((lib().rc_block_norm_backward_workspace(rows, d),), torch.uint8)
-    _launch("rc_block_norm_backward", y.device, stream, t, rows, d, dz.data_ptr(), _ptr(dh), h.data_ptr(),
+    _launch("rc_block_norm_backward", dev, stream, t, rows, d, dz.data_ptr(), _ptr(dh), h.data_ptr(),
             stats.data_ptr(), y.data_ptr(), wt, _ptr(post_weight), mode, _ptr(gate), pre_weight.data_ptr(),
             residual_scale, dy.data_ptr(), dr.data_ptr(), dpre.data_ptr(), _ptr(dpost), _ptr(dgate), ws.data_ptr())
     return dy, dr, dpre, dpost, dgate
@@ -598,13 +607,8 @@ def grad_norm_clip(grads, max_norm: float, scale: float = 1.0, eps: float = 1e-6
             raise ValueError("each tensor of out must hold as many values as its gradient")
     halves = memoryview(desc).cast("B").cast("I")
     halves[6::8], halves[7::8] = types, out_types
-    if norm is None:
-        norm = _mine(torch.empty(1, dtype=torch.float32, device=dev), stream)
-    _check_dev(norm, "norm")
-    _same_device(dev, ("norm", norm))
-    if norm.dtype != torch.float32 or norm.numel() < 1:
-        raise ValueError("norm must hold one float32 value")
-    ws = _mine(torch.empty((_lib or lib()).rc_grad_norm_clip_workspace(), dtype=torch.uint8, device=dev), stream)
+    norm = _result(norm, (1,), torch.float32, dev, stream, "norm")
+    ws = _result(None, ((_lib or lib()).rc_grad_norm_clip_workspace(),), torch.uint8, dev, stream, "")
     _launch("rc_grad_norm_clip", dev, stream, desc.buffer_info()[0], len(grads), scale, max_norm, eps, ws.data_ptr(),
             norm.data_ptr())
     return norm
