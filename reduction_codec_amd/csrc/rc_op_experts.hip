@@ -543,7 +543,7 @@ template <int SB>
 __device__ __forceinline__ uint32_t span_at(uint32_t r, uint32_t c) { return r * (SB * 64) + ((c ^ (r & 15)) << 4); }
 
 template <int DT, int MF, int NF, int WN, int SB, bool SPANS>
-__global__ __launch_bounds__(64 * WN) void grouped_slim_kernel(const Grouped a, unsigned cols)
+__global__ __launch_bounds__(64 * WN, 2) void grouped_slim_kernel(const Grouped a, unsigned cols)
 {
     constexpr int P = Terms<DT>::v, ES = Elem<DT>::size, RU = DT == kF32 ? 2 : 1, S = SB / 4, T = 64 * WN;
     constexpr uint32_t kOut = 0xFFFFFF00u, PLANE = 16 * MF * SB * 64, BUF = P * PLANE;
@@ -623,37 +623,43 @@ __global__ __launch_bounds__(64 * WN) void grouped_slim_kernel(const Grouped a, 
         }
     };
     auto products = [&](const Span& w, const uint8_t* buf) {
+        // one step is 32 of the contraction; in large tiles its successor's fragments are read and decoded during
+        // its products (the registers would halve the waves of smaller ones)
+        constexpr int AHEAD = MF * NF >= 16 ? 1 : 0, SETS = AHEAD + 1;
+        u32x4 t[SETS][MF][P], v[SETS][NF], codes[NF];
+        uint32_t scale[NF][4];
+        auto fetch = [&](int step) {
+            const int s = step / 4, j = step % 4;
 #pragma unroll
-        for (int s = 0; s < S; ++s) {
-            u32x4 codes[NF];
-            uint32_t scale[NF][4];
+            for (int i = 0; i < MF; ++i)
 #pragma unroll
-            for (int f = 0; f < NF; ++f) {
-                codes[f] = exchange(w.codes[f][s]);
-                if constexpr (SPANS) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) scale[f][j] = w.scale[f][s] >> (8 * j) & 255u;
-                } else {
-                    spread(w.scale[f][s], scale[f]);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                u32x4 t[MF][P];
-#pragma unroll
-                for (int i = 0; i < MF; ++i)
-#pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        t[i][p] = *reinterpret_cast<const u32x4*>(buf + p * PLANE + span_at<SB>(16 * i + m, 16 * s + 4 * j + q));
+                for (int p = 0; p < P; ++p)
+                    t[step % SETS][i][p] = *reinterpret_cast<const u32x4*>(buf + p * PLANE + span_at<SB>(16 * i + m, 4 * step + q));
+            if (j == 0) {
 #pragma unroll
                 for (int f = 0; f < NF; ++f) {
-                    const u32x4 v = decode8(codes[f][j], __uint_as_float(scale[f][j] << 23));
+                    codes[f] = exchange(w.codes[f][s]);
+                    if constexpr (SPANS) {
 #pragma unroll
-                    for (int p = 0; p < P; ++p)
-#pragma unroll
-                        for (int i = 0; i < MF; ++i) acc[f][i] = mfma<false>(v, t[i][p], acc[f][i]);
+                        for (int k = 0; k < 4; ++k) scale[f][k] = w.scale[f][s] >> (8 * k) & 255u;
+                    } else {
+                        spread(w.scale[f][s], scale[f]);
+                    }
                 }
             }
+#pragma unroll
+            for (int f = 0; f < NF; ++f) v[step % SETS][f] = decode8(codes[f][j], __uint_as_float(scale[f][j] << 23));
+        };
+        if (AHEAD) fetch(0);
+#pragma unroll
+        for (int step = 0; step < 4 * S; ++step) {
+            if (step + AHEAD < 4 * S) fetch(step + AHEAD);
+#pragma unroll
+            for (int f = 0; f < NF; ++f)
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int i = 0; i < MF; ++i) acc[f][i] = mfma<false>(v[step % SETS][f], t[step % SETS][i][p], acc[f][i]);
         }
     };
     if (!none) {
@@ -725,28 +731,35 @@ hipError_t launch_tile(const Grouped& a, hipStream_t st)
 // Forward.  The mean rows of an expert choose how many rows a workgroup takes
 // (the weights are read and decoded once per 16 MF rows, but rows that are not
 // there cost as much as others).  bf16, 32 experts of 2048 x 4096, in us with
-// 16, 32, 64, 128 rows: mean 6: 39, 39, 45, -; mean 16: 51, 51, 55, -; mean 64:
-// 114, 87, 83, 105; mean 128: -, -, 124, 136; mean 256: -, -, 208, 196.  Twice
-// the columns pay once there are tiles for several rounds of the card: 16384
-// rows of 8192 x 4096 1.16 ms -> 1.10, but 8192 rows of 2048 x 4096 180 us ->
-// 196.  Few workgroups of the shared form leave the card idle, and the
-// contraction is cut instead: two rows of 4096 x 4096 take 8 us so, 14 us
-// otherwise; 248 workgroups 9.4 and 8.2 us.
+// 16, 32, 64, 128 rows: mean 6: 40, 39, 45, -; mean 16: 51, 51, 55, -; mean 64:
+// 114, 87, 83, 105; mean 128: -, -, 124, 136; mean 256: -, -, 208, 195.  256
+// columns pay once there are tiles for several rounds of the card: 16384 rows
+// of 8192 x 4096 1110 us -> 1073, but 8192 rows of 2048 x 4096 177 -> 192.
+// Terms take LDS and registers, so fp16 and fp32 stay with fewer rows: fp16 at
+// mean 128 with 32 x 128, 32 x 256, 64 x 256: 195, 192, 163; 600 rows of 1000 x
+// 2080 19, 26, 37; fp32 at mean 64 160, 145, 174.  Few workgroups of the shared
+// form leave the card idle, and the contraction is cut instead: two rows of
+// 4096 x 4096 take 8 us so, 14 us otherwise; 248 workgroups 9.4 and 8.2 us.
 template <int DT>
 hipError_t launch_forward(const Grouped& a, hipStream_t st)
 {
-    constexpr int SB = Terms<DT>::v == 1 ? 16 : 8;
+    constexpr int P = Terms<DT>::v, SB = P == 1 ? 16 : 8;
     const size_t mean = (a.rows + a.experts - 1) / a.experts;
-    const size_t groups = std::min(a.rows, a.rows / 16 + (size_t)a.experts) * ((a.n + 127) / 128);
-    if (groups < 192) return launch_thin<DT, 1, 2, 4>(a, st);
+    // workgroups, about, for tiles of so many rows and columns
+    const auto groups = [&](size_t rows, size_t columns) {
+        return std::min(a.rows, a.rows / rows + (size_t)a.experts) * ((a.n + columns - 1) / columns);
+    };
+    if (groups(16, 128) < 192) return launch_thin<DT, 1, 2, 4>(a, st);
     if (mean <= 8) return launch_slim<DT, 1, 1, 8, SB>(a, st);
-    if (mean <= 40) return launch_slim<DT, 2, 1, 8, SB>(a, st);
-    if constexpr (DT != kBF16) {
-        return launch_slim<DT, 4, 2, 8, 4>(a, st);
-    } else {
+    if constexpr (P == 1) {
+        if (mean <= 40) return launch_slim<DT, 2, 1, 8, 16>(a, st);
         if (mean <= 160) return launch_slim<DT, 4, 1, 8, 8>(a, st);
-        if ((a.rows / 128 + a.experts) * ((a.n + 255) / 256) < 1024) return launch_slim<DT, 8, 1, 8, 4>(a, st);
+        if (groups(128, 256) < 1024) return launch_slim<DT, 8, 2, 4, 4>(a, st);
         return launch_slim<DT, 8, 2, 8, 4>(a, st);
+    } else {
+        if (mean <= 40 || groups(64, 256) < 128) return launch_slim<DT, 2, 2, 4, 4>(a, st);
+        if constexpr (P == 2) return launch_slim<DT, 4, 2, 8, 4>(a, st);
+        else return launch_slim<DT, 2, 2, 8, 4>(a, st);
     }
 }
 
