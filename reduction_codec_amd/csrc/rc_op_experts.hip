@@ -89,7 +89,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* off, int experts, int64
 //
 // An operand lies in LDS as its memory has it: "row" (contraction innermost:
 // dy for dx), read with 16-byte loads; or "column" (contraction outermost: the
-// weights for dx, both operands of dW), read with the transposing loads, which
+// weights for dx, both operands of dW, here in fp32), read with the transposing loads, which
 // give lane i column i of four rows.  Both are swizzled (row_at, col_at) so
 // that the lanes of one load fall on all banks.
 //
@@ -211,17 +211,23 @@ __device__ __forceinline__ void store4(void* out, int ot, size_t i, f32x4 v)
     else *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + i) = u32x2{narrow2<kF16>(v[0], v[1]), narrow2<kF16>(v[2], v[3])};
 }
 
-template <int DIR, int DT> struct Planes {
-    // dW in fp16 multiplies fp16 as it is
-    static constexpr int a = (DIR == kDw && DT == kF16) ? 1 : Terms<DT>::v, b = DIR == kDw ? a : 1;
-};
+template <int DIR, int DT> struct Planes { static constexpr int a = Terms<DT>::v, b = DIR == kDw ? a : 1; };
+
+// Tile t of a grid whose workgroups go to the eight XCDs in turn: runs of `run`
+// neighbours (four row tiles, then the next column) stay on one XCD, whose L2
+// then holds what they share, and the runs are dealt to the XCDs in turn, so
+// that experts with many rows load all of them alike.
+__device__ __forceinline__ uint2 tile_of(unsigned block, unsigned run, unsigned cols)
+{
+    const unsigned i = block / 8, t = ((i / run) * 8 + block % 8) * run + i % run;
+    return {t / (4 * cols) * 4 + t % 4, t / 4 % cols};           // row tile, column
+}
 
 template <int DIR, int DT, int BM, int BN, int WM, int WN, int BK = 64>
-__global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Grouped a, unsigned cols)
+__global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Grouped a, unsigned cols, unsigned run)
 {
     constexpr int T = 64 * WM * WN, PA = Planes<DIR, DT>::a, PB = Planes<DIR, DT>::b;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;                 // a wave's fragments
-    constexpr bool F16 = DIR == kDw && DT == kF16;
     constexpr uint32_t A_PLANE = BM * BK * 2, B_PLANE = BN * BK * 2;
     constexpr int UA = BM * BK / 8 / T, UB = BN * BK / (DIR == kDw ? 8 : 32) / T;   // units, or blocks, of a lane
     static_assert(UA >= 1 && UB >= 1 && UA * 8 * T == BM * BK, "tile and threads");
@@ -235,15 +241,17 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
     constexpr int ES = Elem<DT>::size;
     int seg;
     int64_t row, end, depth, m_end;              // the tile's first row, the group's end, the contraction's length
-    const int64_t col = (int64_t)(blockIdx.x % cols) * BN, n_end = kk;
+    const uint2 tile = tile_of(blockIdx.x, run, cols);
+    const int64_t col = (int64_t)tile.y * BN, n_end = kk;
     if constexpr (DIR == kDw) {
-        const unsigned rt = (unsigned)((nn + BM - 1) / BM), t = blockIdx.x / cols;
+        const unsigned rt = (unsigned)((nn + BM - 1) / BM), t = tile.x;
         seg = (int)(t / rt) + 1;
+        if (seg > a.experts) return;
         const Segment g = segment(a.offsets, a.experts, a.rows, seg);
         row = (int64_t)(t % rt) * BM; m_end = nn;
         depth = g.hi - g.lo; end = g.lo;         // `end`: the group's first row
     } else {
-        if (!find_tile<BM>(a.offsets, a.experts, a.rows, blockIdx.x / cols, seg, row, end)) return;
+        if (!find_tile<BM>(a.offsets, a.experts, a.rows, tile.x, seg, row, end)) return;
         m_end = end;
         depth = (seg == 0 || seg > a.experts) ? 0 : nn;   // rows of no expert: zeros
     }
@@ -313,8 +321,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
     for (int f = 0; f < FM; ++f)
         if constexpr (DIR == kDw) at_col_a[f] = col_at<BM>(8 * q + m / 4, (wm * (BM / WM) + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
 #pragma unroll
-    for (int f = 0; f < FN; ++f)
-        at_col_b[f] = col_at<BN>(8 * q + m / 4, (wn * (BN / WN) + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
+    for (int f = 0; f < FN; ++f) at_col_b[f] = col_at<BN>(8 * q + m / 4, (wn * (BN / WN) + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
     auto products = [&](const uint8_t* buf) {
 #pragma unroll
         for (int s = 0; s < BK / 32; ++s) {
@@ -339,7 +346,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
 #pragma unroll
                     for (int i = 0; i < FM; ++i)
 #pragma unroll
-                        for (int j = 0; j < FN; ++j) acc[i][j] = mfma<F16>(fb[j], fa[i], acc[i][j]);
+                        for (int j = 0; j < FN; ++j) acc[i][j] = mfma<false>(fb[j], fa[i], acc[i][j]);
                 }
             }
         }
@@ -367,6 +374,114 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
         for (int j = 0; j < FN; ++j) {
             const int64_t c = col + wn * (BN / WN) + 16 * j + 4 * q;
             if (c < n_end) store4(a.out, a.out_t, obase + (size_t)r * n_end + c, acc[i][j]);
+        }
+    }
+}
+
+// ---- dW in 16-bit types: rows straight to LDS ----------------------------
+//
+// Both operands are rows as they lie in memory, so they need no registers on
+// their way: 32 rows of 256 columns each go to LDS with the buffer loads that
+// write there, into four stages, three of which are in flight while the matrix
+// cores work on the fourth.  A 256 x 256 tile, waves and swizzle as above (the
+// swizzle is in the lanes' memory addresses: LDS is written in lane order).
+// Rows past the group's end and columns past the last one lie past the
+// descriptors' ends and arrive as zeros.
+//
+// 16 experts of 2048 x 4096 in us, against the kernel above with one step in
+// flight: mean 8 rows 99 (104), 64: 113 (127), 512: 222 (257, of which writing
+// the 537 MB takes 84 at the rate of a copy), 2048: 524 (656; 1.05 PFLOP/s).
+// 256 x 128 tiles, two workgroups per unit: 97, 124, 232, 544; stores past the
+// cache 150, 156, 261, 583 (a wave writes 64-byte pieces of 16 rows).
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+template <bool F16>
+__global__ __launch_bounds__(512, 2) void grouped_dw_kernel(const Grouped a, unsigned cols, unsigned run)
+{
+    constexpr int B = 256, BK = 32, FM = 8, FN = 4;
+    constexpr uint32_t kOut = 0xFFFFFF00u, A_BYTES = BK * B * 2, STAGE = 2 * A_BYTES;
+    // arrays of their own: the compiler then knows which loads to LDS a read has to wait for
+    __shared__ __attribute__((aligned(16))) uint8_t s0[STAGE], s1[STAGE], s2[STAGE], s3[STAGE];
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / 4, wn = wave % 4;
+    const uint32_t m = lane & 15, q = lane >> 4;
+    const int64_t nn = a.n, kk = a.k;
+    const uint2 tile = tile_of(blockIdx.x, run, cols);
+    const unsigned rt = (unsigned)((nn + B - 1) / B);
+    const int seg = (int)(tile.x / rt) + 1;
+    if (seg > a.experts) return;
+    const int64_t row = (int64_t)(tile.x % rt) * B, col = (int64_t)tile.y * B;
+    const Segment g = segment(a.offsets, a.experts, a.rows, seg);
+    const int lo = __builtin_amdgcn_readfirstlane((int)g.lo), depth = __builtin_amdgcn_readfirstlane((int)(g.hi - g.lo));   // rows < 2^31
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM * FN; ++i) acc[i / FN][i % FN] = f32x4{0, 0, 0, 0};
+
+    uint32_t off_a[2], off_b[2];                 // the lane's units of a stage, two of each operand
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t s = i * 512 + tid, r = s / (B / 8), c = s % (B / 8) ^ ((r & 3) << 1 | (r & 8));
+        off_a[i] = row + c * 8 < nn ? (r * (uint32_t)nn + c * 8) * 2 : kOut;
+        off_b[i] = col + c * 8 < kk ? (r * (uint32_t)kk + c * 8) * 2 : kOut;
+    }
+    auto load = [&](uint8_t (&stage)[STAGE], int c0) {
+        const int rem = max(min(depth - c0, BK), 0);   // rows of this stage; none: all zeros
+        const size_t at = (size_t)lo + c0;
+        const Rsrc ra = span_rsrc(a.a, (at * nn + row) * 2, __builtin_amdgcn_readfirstlane(max(rem * (int)nn - (int)row, 0) * 2));
+        const Rsrc rb = span_rsrc(a.b, (at * kk + col) * 2, __builtin_amdgcn_readfirstlane(max(rem * (int)kk - (int)col, 0) * 2));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(stage + (i * 512 + wave * 64) * 16), 16, off_a[i], 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(stage + A_BYTES + (i * 512 + wave * 64) * 16), 16, off_b[i], 0, 0, 0);
+        }
+    };
+    uint32_t at_a[FM], at_b[FN];
+#pragma unroll
+    for (int f = 0; f < FM; ++f) at_a[f] = col_at<B>(8 * q + m / 4, (wm * 128 + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
+#pragma unroll
+    for (int f = 0; f < FN; ++f) at_b[f] = A_BYTES + col_at<B>(8 * q + m / 4, (wn * 64 + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
+    // Stage `now` holds step t; `then` was step t - 1's and takes step t + 3.  The wait leaves the 8 loads of steps
+    // t + 1 and t + 2 in flight and ends this wave's reads of `then`; past the barrier that holds for all waves.
+    auto step = [&](uint8_t (&now)[STAGE], uint8_t (&then)[STAGE], int c0) {
+        asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        load(then, c0 + 3 * BK);
+        __builtin_amdgcn_sched_barrier(0);
+        u32x4 fa[FM], fb[FN];
+#pragma unroll
+        for (int f = 0; f < FN; ++f) fb[f] = load_columns(now + at_b[f], 4 * B * 2);
+#pragma unroll
+        for (int f = 0; f < FM; ++f) fa[f] = load_columns(now + at_a[f], 4 * B * 2);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = mfma<F16>(fb[j], fa[i], acc[i][j]);
+    };
+    if (depth > 0) {
+        load(s0, 0);
+        load(s1, BK);
+        load(s2, 2 * BK);
+        int c0 = 0;
+        for (; c0 + 4 * BK <= depth; c0 += 4 * BK) {       // without exits in between: those would make the compiler wait for more
+            step(s0, s3, c0);
+            step(s1, s0, c0 + BK);
+            step(s2, s1, c0 + 2 * BK);
+            step(s3, s2, c0 + 3 * BK);
+        }
+        if (c0 < depth) step(s0, s3, c0);
+        if (c0 + BK < depth) step(s1, s0, c0 + BK);
+        if (c0 + 2 * BK < depth) step(s2, s1, c0 + 2 * BK);
+        if (c0 + 3 * BK < depth) step(s3, s2, c0 + 3 * BK);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing writes to LDS after the workgroup's end
+    }
+    const size_t obase = (size_t)(seg - 1) * nn * kk;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int64_t r = row + wm * 128 + 16 * i + m;
+        if (r >= nn) continue;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const int64_t c = col + wn * 64 + 16 * j + 4 * q;
+            if (c < kk) store4(a.out, a.out_t, obase + (size_t)r * kk + c, acc[i][j]);
         }
     }
 }
@@ -718,13 +833,27 @@ hipError_t launch_tile(const Grouped& a, hipStream_t st)
     const size_t cols = (a.k + BN - 1) / BN;
     const size_t some = a.rows < (size_t)a.experts + 2 ? a.rows : (size_t)a.experts + 2;   // segments that end inside a tile
     const size_t tiles = DIR == kDw ? (size_t)((a.n + BM - 1) / BM) * a.experts : a.rows / BM + some;
-    if (tiles > kMaxGrid / cols) return hipErrorInvalidConfiguration;
+    if (tiles > (kMaxGrid - 8192) / cols / 4) return hipErrorInvalidConfiguration;
+    const size_t total = (tiles + 3) / 4 * 4 * cols;
+    const unsigned run = 32;
+    const size_t grid = (total + 8 * run - 1) / (8 * run) * (8 * run);
     const auto kernel = &grouped_tile_kernel<DIR, DT, BM, BN, WM, WN, BK>;
     if (bytes > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles * cols)), dim3(64 * WM * WN), bytes, st, a, (unsigned)cols);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * WM * WN), bytes, st, a, (unsigned)cols, run);
+    return hipGetLastError();
+}
+
+template <bool F16>
+hipError_t launch_dw(const Grouped& a, hipStream_t st)
+{
+    const size_t cols = (a.k + 255) / 256, tiles = (size_t)((a.n + 255) / 256) * a.experts;
+    if (tiles > (kMaxGrid - 8192) / cols / 4) return hipErrorInvalidConfiguration;
+    const unsigned run = 32;
+    const size_t total = (tiles + 3) / 4 * 4 * cols, grid = (total + 8 * run - 1) / (8 * run) * (8 * run);
+    hipLaunchKernelGGL((grouped_dw_kernel<F16>), dim3((unsigned)grid), dim3(512), 0, st, a, (unsigned)cols, run);
     return hipGetLastError();
 }
 
@@ -763,11 +892,11 @@ hipError_t launch_forward(const Grouped& a, hipStream_t st)
     }
 }
 
-// Gradients: small tiles until there are rows enough to fill large ones.  dx,
+// Gradients.  dx: small tiles until there are rows enough to fill large ones;
 // 16 experts of 2048 x 4096 in bf16, in us with 64 x 128, 128 x 128, 256 x 256:
-// mean 8: 32, 41, 67; mean 64: 43, 58, 69; mean 512: 221, 207, 215; mean 2048:
-// 799, 684, 639.  dW, 128 x 128 and 256 x 256: mean 8: 105, 128; mean 64: 136,
-// 136; mean 512: 297, 262.
+// mean 8: 30, 41, 67; mean 64: 41, 58, 69; mean 512: 221, 205, 215; mean 2048:
+// 799, 684, 642.  fp16 with 64 x 128 and 128 x 256: mean 64 87, 123; mean 512
+// 440, 381.
 template <int DIR, int DT>
 hipError_t launch_backward(const Grouped& a, hipStream_t st)
 {
@@ -782,8 +911,7 @@ hipError_t launch_backward(const Grouped& a, hipStream_t st)
     } else if constexpr (DT == kF32) {
         return launch_tile<DIR, DT, 128, 128, 2, 4, 32>(a, st);
     } else {
-        if (mean <= 64) return launch_tile<DIR, DT, 128, 128, 2, 2>(a, st);
-        return launch_tile<DIR, DT, 256, 256, 2, 4>(a, st);
+        return launch_dw<DT == kF16>(a, st);
     }
 }
 
