@@ -10,13 +10,15 @@
 // included), so weights are decoded without rounding.  Rows in fp16 and fp32
 // are cut into P = 2 and 3 bfloat16 terms that add up to them exactly, one
 // product per term (dW in fp32: the six products of two terms that reach
-// 2^-22 of the whole; fp16 is multiplied as it is); all sums are binary32.
+// 2^-22 of the whole).  fp16 rows are multiplied as they are in dW, and
+// forward where fp16 holds all weights.  All sums are binary32.
 //
 // The groups' bounds are read by the kernels: a tile index is mapped to its
 // expert by a wave-wide scan of the bounds, and a grid for the largest number
 // of tiles that the sizes allow is launched (surplus workgroups end at once).
 // Bounds are clamped to the rows there are, so no bounds can reach outside.
 #include <algorithm>
+#include <type_traits>
 #include "rc_op.hpp"
 #include "rc_op_launch.hpp"
 
@@ -180,6 +182,19 @@ __device__ __forceinline__ u32x4 decode8(uint32_t codes, float s)
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 2)),
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 3))};
 }
+
+// Eight codes as fp16: exact for scales that in_f16() lets through.
+__device__ __forceinline__ u32x4 decode8_f16(uint32_t codes, float s)
+{
+    return u32x4{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, s, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, s, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, s, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(codes, s, 3))};
+}
+
+// Whether a block of this scale holds normal fp16 values: 0.5 * 2^e >= 2^-14
+// and 6 * 2^e <= 65504.
+__device__ __forceinline__ bool in_f16(uint32_t scale) { return scale - 114u <= 26u; }
 
 template <bool F16>
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
@@ -660,8 +675,8 @@ __device__ __forceinline__ uint32_t span_at(uint32_t r, uint32_t c) { return r *
 template <int DT, int MF, int NF, int WN, int SB, bool SPANS>
 __global__ __launch_bounds__(64 * WN, 2) void grouped_slim_kernel(const Grouped a, unsigned cols)
 {
-    constexpr int P = Terms<DT>::v, ES = Elem<DT>::size, RU = DT == kF32 ? 2 : 1, S = SB / 4, T = 64 * WN;
-    constexpr uint32_t kOut = 0xFFFFFF00u, PLANE = 16 * MF * SB * 64, BUF = P * PLANE;
+    constexpr int L = DT == kF32 ? 3 : 1, ES = Elem<DT>::size, RU = DT == kF32 ? 2 : 1, S = SB / 4, T = 64 * WN;
+    constexpr uint32_t kOut = 0xFFFFFF00u, PLANE = 16 * MF * SB * 64, BUF = L * PLANE;
     constexpr int UX = 16 * MF * SB * 4 / T;         // 16-byte units of a lane
     static_assert(UX * T == 16 * MF * SB * 4, "units and threads");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -731,25 +746,32 @@ __global__ __launch_bounds__(64 * WN, 2) void grouped_slim_kernel(const Grouped 
 #pragma unroll
         for (int i = 0; i < UX; ++i) {
             const uint32_t s = i * T + tid;
-            u32x4 t[P];
-            cut_unit<DT, P>(u[i], t);
+            u32x4 t[L];
+            cut_unit<DT, L>(u[i], t);
 #pragma unroll
-            for (int p = 0; p < P; ++p) *reinterpret_cast<u32x4*>(buf + p * PLANE + span_at<SB>(s / (SB * 4), s % (SB * 4))) = t[p];
+            for (int p = 0; p < L; ++p) *reinterpret_cast<u32x4*>(buf + p * PLANE + span_at<SB>(s / (SB * 4), s % (SB * 4))) = t[p];
         }
     };
-    auto products = [&](const Span& w, const uint8_t* buf) {
+    auto products = [&](const Span& w, const uint8_t* buf, auto as_f16) {
+        constexpr bool F16 = decltype(as_f16)::value;
+        constexpr int P = F16 ? 1 : Terms<DT>::v;
         // one step is 32 of the contraction; in large tiles its successor's fragments are read and decoded during
         // its products (the registers would halve the waves of smaller ones)
-        constexpr int AHEAD = MF * NF >= 16 ? 1 : 0, SETS = AHEAD + 1;
+        constexpr int AHEAD = MF * NF >= 16 && P == L ? 1 : 0, SETS = AHEAD + 1;
         u32x4 t[SETS][MF][P], v[SETS][NF], codes[NF];
         uint32_t scale[NF][4];
         auto fetch = [&](int step) {
             const int s = step / 4, j = step % 4;
 #pragma unroll
-            for (int i = 0; i < MF; ++i)
+            for (int i = 0; i < MF; ++i) {
+                const uint8_t* at = buf + span_at<SB>(16 * i + m, 4 * step + q);
+                if constexpr (L == P) {
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    t[step % SETS][i][p] = *reinterpret_cast<const u32x4*>(buf + p * PLANE + span_at<SB>(16 * i + m, 4 * step + q));
+                    for (int p = 0; p < P; ++p) t[step % SETS][i][p] = *reinterpret_cast<const u32x4*>(at + p * PLANE);
+                } else {
+                    cut_unit<DT, P>(Unit<DT>{*reinterpret_cast<const u32x4*>(at)}, t[step % SETS][i]);
+                }
+            }
             if (j == 0) {
 #pragma unroll
                 for (int f = 0; f < NF; ++f) {
@@ -763,7 +785,10 @@ __global__ __launch_bounds__(64 * WN, 2) void grouped_slim_kernel(const Grouped 
                 }
             }
 #pragma unroll
-            for (int f = 0; f < NF; ++f) v[step % SETS][f] = decode8(codes[f][j], __uint_as_float(scale[f][j] << 23));
+            for (int f = 0; f < NF; ++f) {
+                const float two_e = __uint_as_float(scale[f][j] << 23);
+                v[step % SETS][f] = F16 ? decode8_f16(codes[f][j], two_e) : decode8(codes[f][j], two_e);
+            }
         };
         if (AHEAD) fetch(0);
 #pragma unroll
@@ -774,11 +799,11 @@ __global__ __launch_bounds__(64 * WN, 2) void grouped_slim_kernel(const Grouped 
 #pragma unroll
                 for (int p = 0; p < P; ++p)
 #pragma unroll
-                    for (int i = 0; i < MF; ++i) acc[f][i] = mfma<false>(v[step % SETS][f], t[step % SETS][i][p], acc[f][i]);
+                    for (int i = 0; i < MF; ++i) acc[f][i] = mfma<F16>(v[step % SETS][f], t[step % SETS][i][p], acc[f][i]);
         }
     };
-    if (!none) {
-        // the rows' next span is asked for before the next weights, so it can be stored while those are in flight
+    // the rows' next span is asked for before the next weights, so it can be stored while those are in flight
+    auto run = [&](auto as_f16) {
         Span w0, w1;
         load_rows(0);
         load_weights(w0, 0);
@@ -788,16 +813,39 @@ __global__ __launch_bounds__(64 * WN, 2) void grouped_slim_kernel(const Grouped 
             load_rows(b + SB);
             load_weights(w1, b + SB);
             __builtin_amdgcn_sched_barrier(0);
-            products(w0, lds);
+            products(w0, lds, as_f16);
             store_rows(lds + BUF);
             __syncthreads();
             load_rows(b + 2 * SB);
             load_weights(w0, b + 2 * SB);
             __builtin_amdgcn_sched_barrier(0);
-            products(w1, lds + BUF);
+            products(w1, lds + BUF, as_f16);
             store_rows(lds);
             __syncthreads();
         }
+    };
+    if constexpr (DT == kF16 && MF > 1) {
+        if (!none) {
+            // fp16 rows are multiplied as they are, once, where fp16 holds all the weights: every scale of the tiles
+            // that the workgroup's weight rows lie in is looked at (16 tiles at a time, 16 bytes a lane).  Not with
+            // few rows, where the weights' bytes count and not the products (192 rows: 39 us, 45 with the look).
+            __shared__ uint32_t odd;
+            if (tid == 0) odd = 0;
+            __syncthreads();
+            bool fits = true;
+            const uint32_t tiles = live ? (skip + wrows * blocks + 63) / 64 : 0;
+            for (uint32_t i = lane / 4; i < tiles; i += 16) {
+                const u32x4 x = __builtin_amdgcn_raw_buffer_load_b128(wr, i * 1088 + 1024 + lane % 4 * 16, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) fits = fits && in_f16(x[e / 4] >> (8 * (e % 4)) & 255u);
+            }
+            if (!fits) odd = 1;
+            __syncthreads();
+            if (odd) run(std::false_type{});
+            else run(std::true_type{});
+        }
+    } else {
+        if (!none) run(std::false_type{});
     }
 #pragma unroll
     for (int f = 0; f < NF; ++f)
@@ -811,7 +859,7 @@ __global__ __launch_bounds__(64 * WN, 2) void grouped_slim_kernel(const Grouped 
 template <int DT, int MF, int NF, int WN, int SB>
 hipError_t launch_slim(const Grouped& a, hipStream_t st)
 {
-    constexpr size_t bytes = 2 * (size_t)Terms<DT>::v * 16 * MF * SB * 64;
+    constexpr size_t bytes = 2 * (size_t)(DT == kF32 ? 3 : 1) * 16 * MF * SB * 64;
     static_assert(bytes <= 160 * 1024, "LDS");
     const size_t cols = (a.n + 16 * NF * WN - 1) / (16 * NF * WN), some = a.rows < (size_t)a.experts + 2 ? a.rows : (size_t)a.experts + 2;
     const size_t tiles = a.rows / (16 * MF) + some;
@@ -859,20 +907,22 @@ hipError_t launch_dw(const Grouped& a, hipStream_t st)
 
 // Forward.  The mean rows of an expert choose how many rows a workgroup takes
 // (the weights are read and decoded once per 16 MF rows, but rows that are not
-// there cost as much as others).  bf16, 32 experts of 2048 x 4096, in us with
-// 16, 32, 64, 128 rows: mean 6: 40, 39, 45, -; mean 16: 51, 51, 55, -; mean 64:
-// 114, 87, 83, 105; mean 128: -, -, 124, 136; mean 256: -, -, 208, 195.  256
-// columns pay once there are tiles for several rounds of the card: 16384 rows
-// of 8192 x 4096 1110 us -> 1073, but 8192 rows of 2048 x 4096 177 -> 192.
-// Terms take LDS and registers, so fp16 and fp32 stay with fewer rows: fp16 at
-// mean 128 with 32 x 128, 32 x 256, 64 x 256: 195, 192, 163; 600 rows of 1000 x
-// 2080 19, 26, 37; fp32 at mean 64 160, 145, 174.  Few workgroups of the shared
-// form leave the card idle, and the contraction is cut instead: two rows of
-// 4096 x 4096 take 8 us so, 14 us otherwise; 248 workgroups 9.4 and 8.2 us.
+// there cost as much as others), the number of workgroups how they are cut.
+// bf16, 32 experts of 2048 x 4096, in us with 16, 32, 64, 128 rows: mean 6: 40,
+// 39, 45, -; mean 16: 51, 51, 55, -; mean 64: 114, 87, 83, 105; mean 128: -, -,
+// 124, 130; mean 256: -, -, 208, 194.  128 x 256 tiles pay once there are
+// several rounds of them: 16384 rows of 8192 x 4096 1110 us -> 1073, but 8192
+// rows of 2048 x 4096 177 -> 192.  With few workgroups more and smaller ones:
+// 600 rows of 1000 x 2080 15 us with 32 rows, 22 with 64; 2331 and 6000 rows 27
+// and 45 with 64 x 256, 30 and 48 with 128 x 128, 33 and 59 with 64 x 128.
+// Three terms take LDS and registers, so fp32 stays with 32 rows: mean 64 with
+// 32 x 128, 32 x 256, 64 x 256: 160, 145, 174.  Fewer still leave the card
+// idle, and the contraction is cut instead: two rows of 4096 x 4096 take 8 us
+// so, 14 us otherwise; 248 workgroups 9.4 and 8.2 us.
 template <int DT>
 hipError_t launch_forward(const Grouped& a, hipStream_t st)
 {
-    constexpr int P = Terms<DT>::v, SB = P == 1 ? 16 : 8;
+    constexpr int SB = DT == kF32 ? 8 : 16;
     const size_t mean = (a.rows + a.experts - 1) / a.experts;
     // workgroups, about, for tiles of so many rows and columns
     const auto groups = [&](size_t rows, size_t columns) {
@@ -880,15 +930,16 @@ hipError_t launch_forward(const Grouped& a, hipStream_t st)
     };
     if (groups(16, 128) < 192) return launch_thin<DT, 1, 2, 4>(a, st);
     if (mean <= 8) return launch_slim<DT, 1, 1, 8, SB>(a, st);
-    if constexpr (P == 1) {
+    if constexpr (DT != kF32) {
         if (mean <= 40) return launch_slim<DT, 2, 1, 8, 16>(a, st);
+        if (groups(64, 128) < 256) return launch_slim<DT, 2, 1, 8, 8>(a, st);
         if (mean <= 160) return launch_slim<DT, 4, 1, 8, 8>(a, st);
+        if (groups(64, 256) < 768) return launch_slim<DT, 4, 2, 8, 4>(a, st);
         if (groups(128, 256) < 1024) return launch_slim<DT, 8, 2, 4, 4>(a, st);
         return launch_slim<DT, 8, 2, 8, 4>(a, st);
     } else {
         if (mean <= 40 || groups(64, 256) < 128) return launch_slim<DT, 2, 2, 4, 4>(a, st);
-        if constexpr (P == 2) return launch_slim<DT, 4, 2, 8, 4>(a, st);
-        else return launch_slim<DT, 2, 2, 8, 4>(a, st);
+        return launch_slim<DT, 2, 2, 8, 4>(a, st);
     }
 }
 

@@ -76,6 +76,21 @@ def test_whole_numbers_are_exact_in_every_direction(case, dtype):
     assert torch.equal(dw.cpu().double(), ref.grouped_dw(dy, x, off)[0])
 
 
+@pytest.mark.parametrize("exponents", [(-30, -27), (-16, -12), (12, 16)])
+@pytest.mark.parametrize("case", [2, 3, 4, 6, 7, 8])
+def test_fp16_rows_on_weights_beyond_fp16(case, exponents):
+    """Weights that fp16 cannot hold, or only as subnormals: the products are
+    formed in another way, exact all the same."""
+    counts, n, k = SHAPES[case]
+    print(f"case beyond fp16 {counts[:6]} n={n} k={k} {exponents}", flush=True)
+    off = offsets_of(counts)
+    packed, w = ref.random_packed(len(counts), n, k, case, exponents=exponents)
+    x = exact_inputs(off[-1], k, torch.float16, 100 + case)
+    y = rca.mxfp4_grouped_matmul(on_gpu(x), on_gpu(packed), on_gpu(torch.tensor(off, dtype=torch.int32)), n,
+                                 out_dtype=torch.float32)
+    assert torch.equal(y.cpu().double(), ref.grouped(x, w, off)[0])
+
+
 @pytest.mark.parametrize("out", DTYPES, ids=str)
 @pytest.mark.parametrize("dtype", DTYPES, ids=str)
 @pytest.mark.parametrize("case", [3, 4, 7, 8])
