@@ -238,20 +238,23 @@ __device__ __forceinline__ uint2 tile_of(unsigned block, unsigned run, unsigned 
     return {t / (4 * cols) * 4 + t % 4, t / 4 % cols};           // row tile, column
 }
 
-template <int DIR, int DT, int BM, int BN, int WM, int WN, int BK = 64>
-__global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Grouped a, unsigned cols, unsigned run)
+template <int DIR, int DT, int BM, int BN, int WM, int WN, int BK = 64, int KS = 1>
+__global__ __launch_bounds__(64 * WM * WN * KS) void grouped_tile_kernel(const Grouped a, unsigned cols, unsigned run)
 {
     constexpr int T = 64 * WM * WN, PA = Planes<DIR, DT>::a, PB = Planes<DIR, DT>::b;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;                 // a wave's fragments
     constexpr uint32_t A_PLANE = BM * BK * 2, B_PLANE = BN * BK * 2;
-    constexpr int UA = BM * BK / 8 / T, UB = BN * BK / (DIR == kDw ? 8 : 32) / T;   // units, or blocks, of a lane
-    static_assert(UA >= 1 && UB >= 1 && UA * 8 * T == BM * BK, "tile and threads");
+    constexpr int NB = BN * BK / (DIR == kDw ? 8 : 32);                  // units, or blocks, of the second operand
+    constexpr int UA = BM * BK / 8 / T, UB = (NB + T - 1) / T;          // of a lane
+    static_assert(UA >= 1 && (NB < T || NB % T == 0) && UA * 8 * T == BM * BK, "tile and threads");
     static_assert(DIR == kDw || BK == 64, "row operands");
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr uint32_t BUF = PA * A_PLANE + PB * B_PLANE;
 
-    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave / WN, wn = wave % WN;
+    // KS groups of waves take every KS-th step each, with buffers of their own, and add up in the end
+    const uint32_t part = threadIdx.x / T, tid = threadIdx.x % T, lane = tid & 63, wave = tid >> 6, wm = wave / WN, wn = wave % WN;
     const uint32_t m = lane & 15, q = lane >> 4;
+    uint8_t* const own = lds + part * 2 * BUF;
     const int64_t nn = a.n, kk = a.k;
     constexpr int ES = Elem<DT>::size;
     int seg;
@@ -301,7 +304,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
             } else {                             // block c of W[c0 + r], from column col on
                 const uint32_t r = s / (BN / 32), c = s % (BN / 32);
                 rw[i] = load_block32(a.w, (int64_t)((wbase + (size_t)(c0 + r) * kk + col) / 32 + c),
-                                     c0 + r < nn && col + c * 32 < kk);
+                                     s < NB && c0 + r < nn && col + c * 32 < kk);
             }
         }
     };
@@ -320,6 +323,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
                 store_unit<DT, PB>(buf + col_at<BN>(s / (BN / 8), s % (BN / 8)), B_PLANE, rb[i]);
             } else {
                 const float scale = __uint_as_float(rw[i].scale << 23);
+                if (s >= NB) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t at = col_at<BN>(s / (BN / 32), s % (BN / 32) * 4 + e);
@@ -367,18 +371,32 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
         }
     };
     if (depth > 0) {
-        load(0);
-        store(lds);
+        const int64_t c1 = (int64_t)part * BK;   // this group's first step; all groups go as often, some into zeros
+        load(c1);
+        store(own);
         __syncthreads();
         uint32_t cur = 0;
-        for (int64_t c0 = 0; c0 < depth; c0 += BK) {
-            const bool more = c0 + BK < depth;
-            if (more) load(c0 + BK);
-            products(lds + cur);
+        for (int64_t c0 = 0; c0 < depth; c0 += BK * KS) {
+            const bool more = c0 + BK * KS < depth;
+            if (more) load(c0 + c1 + BK * KS);
+            products(own + cur);
             cur ^= BUF;
-            if (more) store(lds + cur);
+            if (more) store(own + cur);
             __syncthreads();
         }
+    }
+    if constexpr (KS > 1) {                      // the groups' sums, in their order
+        static_assert((KS - 1) * FM * FN * T * 16 <= KS * 2 * BUF, "room for the sums");
+        f32x4* sums = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+        for (int i = 0; i < FM * FN; ++i)
+            if (part > 0) sums[((part - 1) * FM * FN + i) * T + tid] = acc[i / FN][i % FN];
+        __syncthreads();
+        if (part > 0) return;
+#pragma unroll
+        for (int i = 0; i < FM * FN; ++i)
+#pragma unroll
+            for (int p = 0; p < KS - 1; ++p) acc[i / FN][i % FN] += sums[(p * FM * FN + i) * T + tid];
     }
     const size_t obase = DIR == kDw ? wbase : 0;
 #pragma unroll
@@ -396,12 +414,13 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
 // ---- dW in 16-bit types: rows straight to LDS ----------------------------
 //
 // Both operands are rows as they lie in memory, so they need no registers on
-// their way: 32 rows of 256 columns each go to LDS with the buffer loads that
+// their way: 32 rows of B columns each go to LDS with the buffer loads that
 // write there, into four stages, three of which are in flight while the matrix
-// cores work on the fourth.  A 256 x 256 tile, waves and swizzle as above (the
-// swizzle is in the lanes' memory addresses: LDS is written in lane order).
+// cores work on the fourth.  A B x B tile, swizzled as above (the swizzle
+// is in the lanes' memory addresses: LDS is written in lane order).
 // Rows past the group's end and columns past the last one lie past the
-// descriptors' ends and arrive as zeros.
+// descriptors' ends and arrive as zeros.  128 x 128 tiles of four waves where
+// large ones are few.
 //
 // 16 experts of 2048 x 4096 in us, against the kernel above with one step in
 // flight: mean 8 rows 99 (104), 64: 113 (127), 512: 222 (257, of which writing
@@ -411,14 +430,14 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_tile_kernel(const Groupe
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-template <bool F16>
-__global__ __launch_bounds__(512, 2) void grouped_dw_kernel(const Grouped a, unsigned cols, unsigned run)
+template <bool F16, int B>
+__global__ __launch_bounds__(2 * B, 2) void grouped_dw_kernel(const Grouped a, unsigned cols, unsigned run)
 {
-    constexpr int B = 256, BK = 32, FM = 8, FN = 4;
+    constexpr int BK = 32, WN = B / 64, FM = B / 32, FN = 4, T = 2 * B;   // waves of B / 2 rows by 64 columns
     constexpr uint32_t kOut = 0xFFFFFF00u, A_BYTES = BK * B * 2, STAGE = 2 * A_BYTES;
     // arrays of their own: the compiler then knows which loads to LDS a read has to wait for
     __shared__ __attribute__((aligned(16))) uint8_t s0[STAGE], s1[STAGE], s2[STAGE], s3[STAGE];
-    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / 4, wn = wave % 4;
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / WN, wn = wave % WN;
     const uint32_t m = lane & 15, q = lane >> 4;
     const int64_t nn = a.n, kk = a.k;
     const uint2 tile = tile_of(blockIdx.x, run, cols);
@@ -435,7 +454,7 @@ __global__ __launch_bounds__(512, 2) void grouped_dw_kernel(const Grouped a, uns
     uint32_t off_a[2], off_b[2];                 // the lane's units of a stage, two of each operand
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint32_t s = i * 512 + tid, r = s / (B / 8), c = s % (B / 8) ^ ((r & 3) << 1 | (r & 8));
+        const uint32_t s = i * T + tid, r = s / (B / 8), c = s % (B / 8) ^ ((r & 3) << 1 | (r & 8));
         off_a[i] = row + c * 8 < nn ? (r * (uint32_t)nn + c * 8) * 2 : kOut;
         off_b[i] = col + c * 8 < kk ? (r * (uint32_t)kk + c * 8) * 2 : kOut;
     }
@@ -446,13 +465,13 @@ __global__ __launch_bounds__(512, 2) void grouped_dw_kernel(const Grouped a, uns
         const Rsrc rb = span_rsrc(a.b, (at * kk + col) * 2, __builtin_amdgcn_readfirstlane(max(rem * (int)kk - (int)col, 0) * 2));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(stage + (i * 512 + wave * 64) * 16), 16, off_a[i], 0, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(stage + A_BYTES + (i * 512 + wave * 64) * 16), 16, off_b[i], 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (lds_void*)(stage + (i * T + wave * 64) * 16), 16, off_a[i], 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (lds_void*)(stage + A_BYTES + (i * T + wave * 64) * 16), 16, off_b[i], 0, 0, 0);
         }
     };
     uint32_t at_a[FM], at_b[FN];
 #pragma unroll
-    for (int f = 0; f < FM; ++f) at_a[f] = col_at<B>(8 * q + m / 4, (wm * 128 + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
+    for (int f = 0; f < FM; ++f) at_a[f] = col_at<B>(8 * q + m / 4, (wm * (B / 2) + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
 #pragma unroll
     for (int f = 0; f < FN; ++f) at_b[f] = A_BYTES + col_at<B>(8 * q + m / 4, (wn * 64 + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
     // Stage `now` holds step t; `then` was step t - 1's and takes step t + 3.  The wait leaves the 8 loads of steps
@@ -491,7 +510,7 @@ __global__ __launch_bounds__(512, 2) void grouped_dw_kernel(const Grouped a, uns
     const size_t obase = (size_t)(seg - 1) * nn * kk;
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-        const int64_t r = row + wm * 128 + 16 * i + m;
+        const int64_t r = row + wm * (B / 2) + 16 * i + m;
         if (r >= nn) continue;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
@@ -873,35 +892,44 @@ hipError_t launch_slim(const Grouped& a, hipStream_t st)
     return hipGetLastError();
 }
 
-template <int DIR, int DT, int BM, int BN, int WM, int WN, int BK = 64>
+// Workgroups for `tiles` row tiles by `cols` columns and the runs of tile_of;
+// 0 when they are too many.  Runs of 32 tiles where every XCD gets several.
+inline size_t tile_grid(size_t tiles, size_t cols, unsigned& run)
+{
+    if (tiles > (kMaxGrid - 8192) / cols / 4) return 0;
+    const size_t total = (tiles + 3) / 4 * 4 * cols;
+    run = total >= 1024 ? 32 : total >= 256 ? 4 : 1;
+    return (total + 8 * run - 1) / (8 * run) * (8 * run);
+}
+
+template <int DIR, int DT, int BM, int BN, int WM, int WN, int BK = 64, int KS = 1>
 hipError_t launch_tile(const Grouped& a, hipStream_t st)
 {
-    constexpr size_t bytes = 2 * (size_t)(Planes<DIR, DT>::a * BM + Planes<DIR, DT>::b * BN) * BK * 2;
+    constexpr size_t bytes = KS * 2 * (size_t)(Planes<DIR, DT>::a * BM + Planes<DIR, DT>::b * BN) * BK * 2;
     static_assert(bytes <= 160 * 1024, "LDS");
     const size_t cols = (a.k + BN - 1) / BN;
     const size_t some = a.rows < (size_t)a.experts + 2 ? a.rows : (size_t)a.experts + 2;   // segments that end inside a tile
     const size_t tiles = DIR == kDw ? (size_t)((a.n + BM - 1) / BM) * a.experts : a.rows / BM + some;
-    if (tiles > (kMaxGrid - 8192) / cols / 4) return hipErrorInvalidConfiguration;
-    const size_t total = (tiles + 3) / 4 * 4 * cols;
-    const unsigned run = 32;
-    const size_t grid = (total + 8 * run - 1) / (8 * run) * (8 * run);
-    const auto kernel = &grouped_tile_kernel<DIR, DT, BM, BN, WM, WN, BK>;
+    unsigned run;
+    const size_t grid = tile_grid(tiles, cols, run);
+    if (grid == 0) return hipErrorInvalidConfiguration;
+    const auto kernel = &grouped_tile_kernel<DIR, DT, BM, BN, WM, WN, BK, KS>;
     if (bytes > 64 * 1024) {
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * WM * WN), bytes, st, a, (unsigned)cols, run);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * WM * WN * KS), bytes, st, a, (unsigned)cols, run);
     return hipGetLastError();
 }
 
-template <bool F16>
+template <bool F16, int B>
 hipError_t launch_dw(const Grouped& a, hipStream_t st)
 {
-    const size_t cols = (a.k + 255) / 256, tiles = (size_t)((a.n + 255) / 256) * a.experts;
-    if (tiles > (kMaxGrid - 8192) / cols / 4) return hipErrorInvalidConfiguration;
-    const unsigned run = 32;
-    const size_t total = (tiles + 3) / 4 * 4 * cols, grid = (total + 8 * run - 1) / (8 * run) * (8 * run);
-    hipLaunchKernelGGL((grouped_dw_kernel<F16>), dim3((unsigned)grid), dim3(512), 0, st, a, (unsigned)cols, run);
+    const size_t cols = (a.k + B - 1) / B, tiles = (size_t)((a.n + B - 1) / B) * a.experts;
+    unsigned run;
+    const size_t grid = tile_grid(tiles, cols, run);
+    if (grid == 0) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((grouped_dw_kernel<F16, B>), dim3((unsigned)grid), dim3(2 * B), 0, st, a, (unsigned)cols, run);
     return hipGetLastError();
 }
 
@@ -943,26 +971,37 @@ hipError_t launch_forward(const Grouped& a, hipStream_t st)
     }
 }
 
-// Gradients.  dx: small tiles until there are rows enough to fill large ones;
-// 16 experts of 2048 x 4096 in bf16, in us with 64 x 128, 128 x 128, 256 x 256:
-// mean 8: 30, 41, 67; mean 64: 41, 58, 69; mean 512: 221, 205, 215; mean 2048:
-// 799, 684, 642.  fp16 with 64 x 128 and 128 x 256: mean 64 87, 123; mean 512
-// 440, 381.
+// Gradients.  dx: small tiles until there are enough large ones; 16 experts of
+// 2048 x 4096 in bf16, in us with 64 x 128, 128 x 128, 256 x 256: mean 8: 32, 40,
+// 65; mean 64: 43, 58, 69; mean 512: 221, 205, 215; mean 2048: 799, 684, 642;
+// 4282 rows on two experts of 6856 x 256 74, 101, 214.  Very few of them: four
+// groups of waves share the contraction, 37 rows of 3624 x 128 37 -> 19 us, 32
+// rows over 4 experts of 1024 x 1024 12.7 -> 8.2, but 138 tiles 74 -> 80.  fp16
+// with 64 x 128 and 128 x 256: mean 64 67, 108; mean 512 440, 381.
+// dW, 256 x 256 and 128 x 128: 64 large tiles 18, 10; 128: 34, 22; 320: 30, 25;
+// 640: 51, 57; 2048: 222, 267.
 template <int DIR, int DT>
 hipError_t launch_backward(const Grouped& a, hipStream_t st)
 {
-    const size_t mean = (a.rows + a.experts - 1) / a.experts;
-    if constexpr (DIR == kDx && DT == kBF16) {
-        if (mean <= 128) return launch_tile<DIR, DT, 64, 128, 2, 2>(a, st);
-        if (mean <= 768) return launch_tile<DIR, DT, 128, 128, 2, 2>(a, st);
-        return launch_tile<DIR, DT, 256, 256, 2, 4>(a, st);
-    } else if constexpr (DIR == kDx) {
-        if (mean <= 128) return launch_tile<DIR, DT, 64, 128, 2, 2>(a, st);
-        return launch_tile<DIR, DT, 128, 256, 2, 4>(a, st);
+    const size_t experts = (size_t)a.experts, mean = (a.rows + experts - 1) / experts;
+    // workgroups, about, for dx tiles of so many rows and columns
+    [[maybe_unused]] const auto groups = [&](size_t rows, size_t columns) {
+        return std::min(a.rows, a.rows / rows + experts) * ((a.k + columns - 1) / columns);
+    };
+    if constexpr (DIR == kDx) {
+        if (groups(64, 128) < 100) return launch_tile<DIR, DT, 64, 64, 2, 2, 64, DT == kBF16 ? 4 : 2>(a, st);
+        if (mean <= 128 || groups(128, DT == kBF16 ? 128 : 256) < 512) return launch_tile<DIR, DT, 64, 128, 2, 2>(a, st);
+        if constexpr (DT == kBF16) {
+            if (mean <= 768 || groups(256, 256) < 512) return launch_tile<DIR, DT, 128, 128, 2, 2>(a, st);
+            return launch_tile<DIR, DT, 256, 256, 2, 4>(a, st);
+        } else {
+            return launch_tile<DIR, DT, 128, 256, 2, 4>(a, st);
+        }
     } else if constexpr (DT == kF32) {
         return launch_tile<DIR, DT, 128, 128, 2, 4, 32>(a, st);
     } else {
-        return launch_dw<DT == kF16>(a, st);
+        if ((size_t)((a.n + 255) / 256) * ((a.k + 255) / 256) * experts < 512) return launch_dw<DT == kF16, 128>(a, st);
+        return launch_dw<DT == kF16, 256>(a, st);
     }
 }
 
