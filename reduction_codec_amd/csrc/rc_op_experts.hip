@@ -520,6 +520,122 @@ __global__ __launch_bounds__(2 * B, 2) void grouped_dw_kernel(const Grouped a, u
     }
 }
 
+// ---- dx in bf16: dy straight to LDS, weights decoded on their way ---------
+//
+// A 128 x 256 tile of eight waves, 32 of the contraction at a time.  dy goes to
+// LDS with the buffer loads that write there, three of four stages ahead; the
+// weights come two steps ahead to registers (half a block a lane), are decoded
+// during the step before theirs into one of two buffers, and are read from it
+// with the transposing loads.  Rows past the group's end, contraction past n
+// and columns past k lie past the descriptors' ends and arrive as zeros.
+//
+// 16 experts of 2048 x 4096 in us, against 128 x 128 and 256 x 256 tiles of the
+// kernel above with one step in flight: mean 256 rows 104 (121), mean 512 169
+// (205, 215), mean 2048 541 (684, 642; now 1.02 PFLOP/s).
+
+__global__ __launch_bounds__(512, 2) void grouped_dx_kernel(const Grouped a, unsigned cols, unsigned run)
+{
+    constexpr int BM = 128, BN = 256, BK = 32, FM = 4, FN = 4;
+    constexpr uint32_t kOut = 0xFFFFFF00u, STAGE = BM * BK * 2, WSTAGE = BK * BN * 2;
+    __shared__ __attribute__((aligned(16))) uint8_t s0[STAGE], s1[STAGE], s2[STAGE], s3[STAGE], d0[WSTAGE], d1[WSTAGE];
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), wm = wave / 4, wn = wave % 4;
+    const uint32_t m = lane & 15, q = lane >> 4;
+    const int64_t nn = a.n, kk = a.k;
+    const uint2 tile = tile_of(blockIdx.x, run, cols);
+    const int64_t col = (int64_t)tile.y * BN;
+    int seg;
+    int64_t row, end;
+    if (!find_tile<BM>(a.offsets, a.experts, a.rows, tile.x, seg, row, end)) return;
+    const int depth = (seg == 0 || seg > a.experts) ? 0 : (int)nn;   // rows of no expert: zeros
+    f32x4 acc[FM][FN];
+#pragma unroll
+    for (int i = 0; i < FM * FN; ++i) acc[i / FN][i % FN] = f32x4{0, 0, 0, 0};
+
+    // dy: unit c of row r, at place c ^ (r / 4 % 4) of the row's four
+    const uint32_t rows = (uint32_t)(end - row < BM ? end - row : BM), r = tid / 4, c = tid % 4 ^ (r >> 2 & 3);
+    const Rsrc dr = span_rsrc(a.a, (size_t)row * nn * 2, rows * (uint32_t)nn * 2);
+    const uint32_t off_r = r < rows ? (r * (uint32_t)nn + c * 8) * 2 : kOut;
+    auto load_rows = [&](uint8_t (&stage)[STAGE], int c0) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(dr, (lds_void*)(stage + wave * 1024), 16,
+                                                 c0 + (int)c * 8 < depth && off_r != kOut ? off_r + c0 * 2 : kOut, 0, 0, 0);
+    };
+    // weights: half h of block b of contraction row wr
+    struct Half { u32x2 codes; uint32_t scale; };
+    const uint32_t wr = tid / 16, b = tid / 2 % 8, h = tid % 2, blocks = (uint32_t)(kk / 32);
+    const uint32_t off_w = col + b * 32 < kk ? wr * blocks + b : kOut;
+    auto load_half = [&](Half& w, int c0) {
+        const int64_t fb = ((int64_t)(seg - 1) * nn + c0) * blocks + col / 32;
+        const Rsrc wd = span_rsrc(a.w, (size_t)(fb >> 6) * 1088, 0x7FFFFFFF);
+        const uint32_t at = off_w + (uint32_t)(fb & 63);
+        const uint32_t out = off_w == kOut || c0 + (int)wr >= depth ? 0xFFFFFFFFu : 0u;   // past the descriptor's end
+        w.codes = __builtin_amdgcn_raw_buffer_load_b64(wd, ((at >> 6) * 1088 + (at & 63) * 16 + h * 8) | out, 0, 0);
+        w.scale = __builtin_amdgcn_raw_buffer_load_b8(wd, ((at >> 6) * 1088 + 1024 + (at & 63)) | out, 0, 0);
+    };
+    auto decode = [&](uint8_t (&buf)[WSTAGE], const Half& w) {
+        const float s = __uint_as_float(w.scale << 23);
+        *reinterpret_cast<u32x4*>(buf + col_at<BN>(wr, b * 4 + h * 2)) = decode8(w.codes.x, s);
+        *reinterpret_cast<u32x4*>(buf + col_at<BN>(wr, b * 4 + h * 2 + 1)) = decode8(w.codes.y, s);
+    };
+    uint32_t at_a = (wm * 64 + m) * 64 + ((q ^ (m >> 2)) << 4), at_b[FN];
+#pragma unroll
+    for (int f = 0; f < FN; ++f) at_b[f] = col_at<BN>(8 * q + m / 4, (wn * 64 + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
+    // Step t: `now` and `w` hold its operands.  Three loads are issued a step, dy's first, so past 8 of them dy of
+    // step t is there; the barrier also ends all waves' reads of `then` (step t - 1) and of `next`.
+    auto step = [&](uint8_t (&now)[STAGE], uint8_t (&then)[STAGE], uint8_t (&w)[WSTAGE], uint8_t (&next)[WSTAGE],
+                    Half& ahead, const Half& coming, int c0) {
+        asm volatile("s_waitcnt vmcnt(8) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        load_rows(then, c0 + 3 * BK);
+        __builtin_amdgcn_sched_barrier(0);
+        load_half(ahead, c0 + 3 * BK);
+        __builtin_amdgcn_sched_barrier(0);
+        u32x4 fa[FM], fb[FN];
+#pragma unroll
+        for (int f = 0; f < FN; ++f) fb[f] = load_columns(w + at_b[f], 4 * BN * 2);
+#pragma unroll
+        for (int f = 0; f < FM; ++f) fa[f] = *reinterpret_cast<const u32x4*>(now + at_a + f * 16 * 64);
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = mfma<false>(fb[j], fa[i], acc[i][j]);
+        __builtin_amdgcn_sched_barrier(0);
+        decode(next, coming);
+    };
+    if (depth > 0) {
+        Half w0, w1, w2, w3;
+        load_half(w0, 0);
+        load_half(w1, BK);
+        load_half(w2, 2 * BK);
+        __builtin_amdgcn_sched_barrier(0);
+        load_rows(s0, 0);
+        load_rows(s1, BK);
+        load_rows(s2, 2 * BK);
+        decode(d0, w0);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the steps count on three loads of each of the last ones
+        int c0 = 0;
+        for (; c0 + 4 * BK <= depth; c0 += 4 * BK) {
+            step(s0, s3, d0, d1, w3, w1, c0);
+            step(s1, s0, d1, d0, w0, w2, c0 + BK);
+            step(s2, s1, d0, d1, w1, w3, c0 + 2 * BK);
+            step(s3, s2, d1, d0, w2, w0, c0 + 3 * BK);
+        }
+        if (c0 < depth) step(s0, s3, d0, d1, w3, w1, c0);
+        if (c0 + BK < depth) step(s1, s0, d1, d0, w0, w2, c0 + BK);
+        if (c0 + 2 * BK < depth) step(s2, s1, d0, d1, w1, w3, c0 + 2 * BK);
+        if (c0 + 3 * BK < depth) step(s3, s2, d1, d0, w2, w0, c0 + 3 * BK);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // nothing writes to LDS after the workgroup's end
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const int64_t o = row + wm * 64 + 16 * i + m;
+        if (o >= end) continue;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+            const int64_t k = col + wn * 64 + 16 * j + 4 * q;
+            if (k < kk) store4(a.out, a.out_t, (size_t)o * kk + k, acc[i][j]);
+        }
+    }
+}
+
 // ---- few rows per expert ------------------------------------------------
 //
 // Forward with a handful of rows per expert is bound by the weights' bytes, so
@@ -933,6 +1049,16 @@ hipError_t launch_dw(const Grouped& a, hipStream_t st)
     return hipGetLastError();
 }
 
+hipError_t launch_dx(const Grouped& a, hipStream_t st)
+{
+    const size_t cols = (a.k + 255) / 256, some = a.rows < (size_t)a.experts + 2 ? a.rows : (size_t)a.experts + 2;
+    unsigned run;
+    const size_t grid = tile_grid(a.rows / 128 + some, cols, run);
+    if (grid == 0) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL(grouped_dx_kernel, dim3((unsigned)grid), dim3(512), 0, st, a, (unsigned)cols, run);
+    return hipGetLastError();
+}
+
 // Forward.  The mean rows of an expert choose how many rows a workgroup takes
 // (the weights are read and decoded once per 16 MF rows, but rows that are not
 // there cost as much as others), the number of workgroups how they are cut.
@@ -971,10 +1097,10 @@ hipError_t launch_forward(const Grouped& a, hipStream_t st)
     }
 }
 
-// Gradients.  dx: small tiles until there are enough large ones; 16 experts of
-// 2048 x 4096 in bf16, in us with 64 x 128, 128 x 128, 256 x 256: mean 8: 32, 40,
-// 65; mean 64: 43, 58, 69; mean 512: 221, 205, 215; mean 2048: 799, 684, 642;
-// 4282 rows on two experts of 6856 x 256 74, 101, 214.  Very few of them: four
+// Gradients.  dx: 64 x 128 tiles until there are enough of 128 x 256; 16 experts
+// of 2048 x 4096 in bf16, in us: mean 8: 33, 40; mean 64: 43, 53; mean 256: 123,
+// 104; mean 512: 225, 169; 4282 rows on two experts of 6856 x 256 74, 126; 4096
+// rows on 8 of 1024 x 1024 (160 large tiles) 25, 27.  Very few: four
 // groups of waves share the contraction, 37 rows of 3624 x 128 37 -> 19 us, 32
 // rows over 4 experts of 1024 x 1024 12.7 -> 8.2, but 138 tiles 74 -> 80.  fp16
 // with 64 x 128 and 128 x 256: mean 64 67, 108; mean 512 440, 381.
@@ -990,13 +1116,9 @@ hipError_t launch_backward(const Grouped& a, hipStream_t st)
     };
     if constexpr (DIR == kDx) {
         if (groups(64, 128) < 100) return launch_tile<DIR, DT, 64, 64, 2, 2, 64, DT == kBF16 ? 4 : 2>(a, st);
-        if (mean <= 128 || groups(128, DT == kBF16 ? 128 : 256) < 512) return launch_tile<DIR, DT, 64, 128, 2, 2>(a, st);
-        if constexpr (DT == kBF16) {
-            if (mean <= 768 || groups(256, 256) < 512) return launch_tile<DIR, DT, 128, 128, 2, 2>(a, st);
-            return launch_tile<DIR, DT, 256, 256, 2, 4>(a, st);
-        } else {
-            return launch_tile<DIR, DT, 128, 256, 2, 4>(a, st);
-        }
+        if (mean <= 128 || groups(128, 256) < 256) return launch_tile<DIR, DT, 64, 128, 2, 2>(a, st);
+        if constexpr (DT == kBF16) return launch_dx(a, st);
+        else return launch_tile<DIR, DT, 128, 256, 2, 4>(a, st);
     } else if constexpr (DT == kF32) {
         return launch_tile<DIR, DT, 128, 128, 2, 4, 32>(a, st);
     } else {
