@@ -108,6 +108,11 @@ __device__ __forceinline__ uint32_t col_at(uint32_t r, uint32_t c)
     return r * (COLS * 2) + ((c ^ (((r & 3) << 1 | (r & 8)) & (COLS / 8 - 1))) << 4);
 }
 
+// col_at for decoded weights.  A lane writes two or four neighbouring units, so eight lanes' first units alone would
+// share a half or a quarter of the banks; each group of eight units is shifted within its fours by its number.
+template <int COLS>
+__device__ __forceinline__ uint32_t weight_at(uint32_t r, uint32_t c) { return col_at<COLS>(r, c ^ (c >> 3 & 3)); }
+
 template <int DT> struct Unit { u32x4 v[DT == kF32 ? 2 : 1]; };        // eight values as they lie in memory
 
 template <int DT>
@@ -326,7 +331,7 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void grouped_tile_kernel(const G
                 if (s >= NB) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t at = col_at<BN>(s / (BN / 32), s % (BN / 32) * 4 + e);
+                    const uint32_t at = weight_at<BN>(s / (BN / 32), s % (BN / 32) * 4 + e);
                     *reinterpret_cast<u32x4*>(buf + at) = decode8(rw[i].codes[e], scale);
                 }
             }
@@ -340,7 +345,10 @@ __global__ __launch_bounds__(64 * WM * WN * KS) void grouped_tile_kernel(const G
     for (int f = 0; f < FM; ++f)
         if constexpr (DIR == kDw) at_col_a[f] = col_at<BM>(8 * q + m / 4, (wm * (BM / WM) + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
 #pragma unroll
-    for (int f = 0; f < FN; ++f) at_col_b[f] = col_at<BN>(8 * q + m / 4, (wn * (BN / WN) + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
+    for (int f = 0; f < FN; ++f) {
+        const uint32_t r = 8 * q + m / 4, c = (wn * (BN / WN) + 16 * f) / 8 + m % 4 / 2;
+        at_col_b[f] = (DIR == kDw ? col_at<BN>(r, c) : weight_at<BN>(r, c)) + m % 2 * 8;
+    }
     auto products = [&](const uint8_t* buf) {
 #pragma unroll
         for (int s = 0; s < BK / 32; ++s) {
@@ -530,8 +538,11 @@ __global__ __launch_bounds__(2 * B, 2) void grouped_dw_kernel(const Grouped a, u
 // and columns past k lie past the descriptors' ends and arrive as zeros.
 //
 // 16 experts of 2048 x 4096 in us, against 128 x 128 and 256 x 256 tiles of the
-// kernel above with one step in flight: mean 256 rows 104 (121), mean 512 169
-// (205, 215), mean 2048 541 (684, 642; now 1.02 PFLOP/s).
+// kernel above with one step in flight: mean 256 rows 99 (121), mean 512 166
+// (205, 215), mean 2048 530 (684, 642; now 1.04 PFLOP/s).  Without the shifts
+// that keep LDS writes of weights and reads of rows free of conflicts 40 % of
+// LDS's active time went to them: 171 and 544; in the kernel above fp16 took
+// 333 for 312.
 
 __global__ __launch_bounds__(512, 2) void grouped_dx_kernel(const Grouped a, unsigned cols, unsigned run)
 {
@@ -551,8 +562,9 @@ __global__ __launch_bounds__(512, 2) void grouped_dx_kernel(const Grouped a, uns
 #pragma unroll
     for (int i = 0; i < FM * FN; ++i) acc[i / FN][i % FN] = f32x4{0, 0, 0, 0};
 
-    // dy: unit c of row r, at place c ^ (r / 4 % 4) of the row's four
-    const uint32_t rows = (uint32_t)(end - row < BM ? end - row : BM), r = tid / 4, c = tid % 4 ^ (r >> 2 & 3);
+    // dy: unit c of row r, at place c ^ (-(r / 4) % 4) of the row's four: the reads take rows 0 .. 3 and 12 .. 15 of one
+    // unit with rows 4 .. 11 of the next, and these fall on all banks
+    const uint32_t rows = (uint32_t)(end - row < BM ? end - row : BM), r = tid / 4, c = tid % 4 ^ (-(r >> 2) & 3);
     const Rsrc dr = span_rsrc(a.a, (size_t)row * nn * 2, rows * (uint32_t)nn * 2);
     const uint32_t off_r = r < rows ? (r * (uint32_t)nn + c * 8) * 2 : kOut;
     auto load_rows = [&](uint8_t (&stage)[STAGE], int c0) {
@@ -573,12 +585,12 @@ __global__ __launch_bounds__(512, 2) void grouped_dx_kernel(const Grouped a, uns
     };
     auto decode = [&](uint8_t (&buf)[WSTAGE], const Half& w) {
         const float s = __uint_as_float(w.scale << 23);
-        *reinterpret_cast<u32x4*>(buf + col_at<BN>(wr, b * 4 + h * 2)) = decode8(w.codes.x, s);
-        *reinterpret_cast<u32x4*>(buf + col_at<BN>(wr, b * 4 + h * 2 + 1)) = decode8(w.codes.y, s);
+        *reinterpret_cast<u32x4*>(buf + weight_at<BN>(wr, b * 4 + h * 2)) = decode8(w.codes.x, s);
+        *reinterpret_cast<u32x4*>(buf + weight_at<BN>(wr, b * 4 + h * 2 + 1)) = decode8(w.codes.y, s);
     };
-    uint32_t at_a = (wm * 64 + m) * 64 + ((q ^ (m >> 2)) << 4), at_b[FN];
+    uint32_t at_a = (wm * 64 + m) * 64 + ((q ^ (-(m >> 2) & 3)) << 4), at_b[FN];
 #pragma unroll
-    for (int f = 0; f < FN; ++f) at_b[f] = col_at<BN>(8 * q + m / 4, (wn * 64 + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
+    for (int f = 0; f < FN; ++f) at_b[f] = weight_at<BN>(8 * q + m / 4, (wn * 64 + 16 * f) / 8 + m % 4 / 2) + m % 2 * 8;
     // Step t: `now` and `w` hold its operands.  Three loads are issued a step, dy's first, so past 8 of them dy of
     // step t is there; the barrier also ends all waves' reads of `then` (step t - 1) and of `next`.
     auto step = [&](uint8_t (&now)[STAGE], uint8_t (&then)[STAGE], uint8_t (&w)[WSTAGE], uint8_t (&next)[WSTAGE],
@@ -1098,12 +1110,13 @@ hipError_t launch_forward(const Grouped& a, hipStream_t st)
 }
 
 // Gradients.  dx: 64 x 128 tiles until there are enough of 128 x 256; 16 experts
-// of 2048 x 4096 in bf16, in us: mean 8: 33, 40; mean 64: 43, 53; mean 256: 123,
-// 104; mean 512: 225, 169; 4282 rows on two experts of 6856 x 256 74, 126; 4096
-// rows on 8 of 1024 x 1024 (160 large tiles) 25, 27.  Very few: four
+// of 2048 x 4096 in bf16, in us: mean 8: 32, 40; mean 64: 45, 53; mean 72: 57,
+// 53; mean 128: 75, 62; mean 256: 125, 99; mean 512: 225, 166; 4282 rows on two experts of 6856 x 256 74, 126; 4096
+// rows on 8 of 1024 x 1024 (160 large tiles) 23, 25.  Very few: four
 // groups of waves share the contraction, 37 rows of 3624 x 128 37 -> 19 us, 32
 // rows over 4 experts of 1024 x 1024 12.7 -> 8.2, but 138 tiles 74 -> 80.  fp16
-// with 64 x 128 and 128 x 256: mean 64 67, 108; mean 512 440, 381.
+// with 64 x 128 and 128 x 256: mean 64 68, 100; mean 128 120, 123; mean 256 196,
+// 187; mean 512 348, 312.
 // dW, 256 x 256 and 128 x 128: 64 large tiles 18, 10; 128: 34, 22; 320: 30, 25;
 // 640: 51, 57; 2048: 222, 267.
 template <int DIR, int DT>
@@ -1116,7 +1129,7 @@ hipError_t launch_backward(const Grouped& a, hipStream_t st)
     };
     if constexpr (DIR == kDx) {
         if (groups(64, 128) < 100) return launch_tile<DIR, DT, 64, 64, 2, 2, 64, DT == kBF16 ? 4 : 2>(a, st);
-        if (mean <= 128 || groups(128, 256) < 256) return launch_tile<DIR, DT, 64, 128, 2, 2>(a, st);
+        if (mean <= (DT == kBF16 ? 64 : 128) || groups(128, 256) < 256) return launch_tile<DIR, DT, 64, 128, 2, 2>(a, st);
         if constexpr (DT == kBF16) return launch_dx(a, st);
         else return launch_tile<DIR, DT, 128, 256, 2, 4>(a, st);
     } else if constexpr (DT == kF32) {
