@@ -1081,6 +1081,9 @@ hipError_t launch_dx(const Grouped& a, hipStream_t st)
 // rows of 2048 x 4096 177 -> 192.  With few workgroups more and smaller ones:
 // 600 rows of 1000 x 2080 15 us with 32 rows, 22 with 64; 2331 and 6000 rows 27
 // and 45 with 64 x 256, 30 and 48 with 128 x 128, 33 and 59 with 64 x 128.
+// There two groups of waves with every second span each did not help (2331 rows
+// 27 us either way in bf16, 28 -> 33 in fp16), nor did waves split over rows
+// too, in any tile (16384 rows 1104 -> 1422).
 // Three terms take LDS and registers, so fp32 stays with 32 rows: mean 64 with
 // 32 x 128, 32 x 256, 64 x 256: 160, 145, 174.  Fewer still leave the card
 // idle, and the contraction is cut instead: two rows of 4096 x 4096 take 8 us
@@ -1111,8 +1114,9 @@ hipError_t launch_forward(const Grouped& a, hipStream_t st)
 
 // Gradients.  dx: 64 x 128 tiles until there are enough of 128 x 256; 16 experts
 // of 2048 x 4096 in bf16, in us: mean 8: 32, 40; mean 64: 45, 53; mean 72: 57,
-// 53; mean 128: 75, 62; mean 256: 125, 99; mean 512: 225, 166; 4282 rows on two experts of 6856 x 256 74, 126; 4096
-// rows on 8 of 1024 x 1024 (160 large tiles) 23, 25.  Very few: four
+// 53; mean 128: 75, 62; mean 256: 125, 99; mean 512: 225, 166; 4282 rows on two
+// experts of 6856 x 256 74, 126; 4096 rows on 8 of 1024 x 1024 (160 large tiles)
+// 23, 25.  Very few: four
 // groups of waves share the contraction, 37 rows of 3624 x 128 37 -> 19 us, 32
 // rows over 4 experts of 1024 x 1024 12.7 -> 8.2, but 138 tiles 74 -> 80.  fp16
 // with 64 x 128 and 128 x 256: mean 64 68, 100; mean 128 120, 123; mean 256 196,
