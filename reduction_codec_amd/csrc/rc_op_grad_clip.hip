@@ -159,7 +159,7 @@ __device__ __forceinline__ void scale_chunk(const Table& t, int k, size_t base, 
     const uint32_t lead = t.lead[k];
     const size_t end = lead + t.n[k];
     u32x4 u[kVecs];
-        load_chunk<DT>(t.in[k], base, lead, end, u);
+    load_chunk<DT>(t.in[k], base, lead, end, u);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const size_t at = base + (size_t)(i * kThreads + threadIdx.x) * E;
@@ -184,7 +184,8 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const Table t, con
     for (uint32_t c = blockIdx.x; c < total; c += gridDim.x) {
         const uint32_t r = total - 1 - c;
         k = tensor_of(t, r, k);
-        if (f == 1.0f && t.in[k] == t.out[k]) continue;   // in place, times one
+        // in place, times one: one type too, for both addresses lie `lead` elements of their own types back
+        if (f == 1.0f && t.in[k] == t.out[k] && t.in_t[k] == t.out_t[k]) continue;
         const size_t base = (size_t)(r - t.first[k]) * chunk_elems(t.in_t[k]);
         if (t.in_t[k] == kF32) scale_chunk<kF32>(t, k, base, f);
         else if (t.in_t[k] == kBF16) scale_chunk<kBF16>(t, k, base, f);
