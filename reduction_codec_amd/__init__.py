@@ -159,12 +159,21 @@ def _same_device(dev: torch.device, *named):
             raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
-def _mine(t: torch.Tensor, stream) -> torch.Tensor:
-    """A tensor this module allocated on the current stream for work enqueued
-    on `stream`: tell torch's caching allocator, so the memory is not handed
-    out again before that stream has finished with it."""
-    if stream is not None and stream != torch.cuda.current_stream(t.device):
-        t.record_stream(stream)
+def _new(shape, dtype: torch.dtype, dev: torch.device, stream) -> torch.Tensor:
+    """A tensor for work enqueued on `stream` (None: the current one), from
+    that stream's memory: a block that the current stream has freed may still
+    be read or written by work queued there, which `stream` does not wait for.
+    The caller goes on with the tensor on the current stream, so torch's
+    allocator is told not to hand it out again before that has finished too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _stream(stream, dev)
+    current = torch.cuda.current_stream(dev)
+    if stream == current:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(current)
     return t
 
 
@@ -198,7 +207,7 @@ def quantize_pack(x: torch.Tensor, codec, out: torch.Tensor | None = None, strea
         raise ValueError(f"unsupported input dtype {x.dtype}")
     n = x.numel()
     if out is None:
-        out = _mine(torch.empty(packed_bytes(c, n), dtype=torch.uint8, device=x.device), stream)
+        out = _new(packed_bytes(c, n), torch.uint8, x.device, stream)
     _check_dev(out, "out")
     _same_device(x.device, ("out", out))
     if out.numel() < packed_bytes(c, n) or out.dtype != torch.uint8:
@@ -220,7 +229,7 @@ def unpack_dequant(packed: torch.Tensor, codec, n: int, dtype: torch.dtype = tor
     if dtype not in _DTYPES:
         raise ValueError(f"unsupported output dtype {dtype}")
     if out is None:
-        out = _mine(torch.empty(n, dtype=dtype, device=packed.device), stream)
+        out = _new(n, dtype, packed.device, stream)
     _check_dev(out, "out")
     _same_device(packed.device, ("out", out))
     if out.numel() < n or out.dtype != dtype:
@@ -249,7 +258,7 @@ def dequant_reduce_requant(streams, codec, n: int, out: torch.Tensor | None = No
             raise ValueError(f"streams[{j}] is shorter than packed_bytes(codec, n)")
     hs = _stream(stream, dev)
     if out is None:
-        out = _mine(torch.empty(need, dtype=torch.uint8, device=dev), stream)
+        out = _new(need, torch.uint8, dev, stream)
     _check_dev(out, "out")
     _same_device(dev, ("out", out))
     if _nbytes(out) < need:
@@ -262,7 +271,7 @@ def dequant_reduce_requant(streams, codec, n: int, out: torch.Tensor | None = No
         if sums.dtype != torch.float32 or sums.numel() < n:
             raise ValueError("sum_out must hold n float32 values")
     elif sum_out:
-        sums = _mine(torch.empty(n, dtype=torch.float32, device=dev), stream)
+        sums = _new(n, torch.float32, dev, stream)
     ptrs = (ctypes.c_void_p * k)(*[s.data_ptr() for s in streams])
     with torch.cuda.device(dev):
         _ok(lib().rc_dequant_reduce_requant(c, ptrs, k, n, out.data_ptr(),
@@ -293,7 +302,7 @@ def allreduce_emulate(msgs, codec, two_shot: bool = True, out: torch.Tensor | No
             raise ValueError("all messages need the same dtype and length")
     hs = _stream(stream, dev)
     if out is None:
-        out = _mine(torch.empty(n, dtype=dt, device=dev), stream)
+        out = _new(n, dt, dev, stream)
     _check_dev(out, "out")
     _same_device(dev, ("out", out))
     if out.dtype != dt or out.numel() < n:
@@ -306,7 +315,7 @@ def allreduce_emulate(msgs, codec, two_shot: bool = True, out: torch.Tensor | No
         if packed.numel() < packed_bytes(c, n) or packed.dtype != torch.uint8:
             raise ValueError("packed_out must be a uint8 tensor of packed_bytes(codec, n) bytes")
     elif packed_out:
-        packed = _mine(torch.empty(packed_bytes(c, n), dtype=torch.uint8, device=dev), stream)
+        packed = _new(packed_bytes(c, n), torch.uint8, dev, stream)
     ptrs = (ctypes.c_void_p * k)(*[m.data_ptr() for m in msgs])
     with torch.cuda.device(dev):
         _ok(lib().rc_allreduce_emulate(c, _DTYPES[dt], ptrs, k, n, 1 if two_shot else 0, out.data_ptr(),
@@ -330,7 +339,7 @@ def mxfp4_gemv(w_packed: torch.Tensor, rows: int, cols: int, x: torch.Tensor, ou
     if out_dtype not in _DTYPES:
         raise ValueError(f"unsupported output dtype {out_dtype}")
     if out is None:
-        out = _mine(torch.empty(rows, dtype=out_dtype, device=x.device), stream)
+        out = _new(rows, out_dtype, x.device, stream)
     _check_dev(out, "out")
     _same_device(w_packed.device, ("out", out))
     if out.dtype != out_dtype or out.numel() < rows:
@@ -373,8 +382,7 @@ def _check_on(t: torch.Tensor, name: str, index: int):
 def _result(out, shape, dtype, dev: torch.device, stream, name: str) -> torch.Tensor:
     """The caller's output, checked, or a new one for work on `stream`."""
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=dev)
-        return out if stream is None else _mine(out, stream)
+        return _new(shape, dtype, dev, stream)
     _check_on(out, name, dev.index)
     if out.dtype != dtype or tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
