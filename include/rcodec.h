@@ -280,7 +280,8 @@ rc_status rc_block_norm_backward(rc_dtype t, size_t rows, size_t d, const void *
  * their elements only (they may be parts of one buffer).  The squares are added
  * in FP64 in an order that the sizes fix.  A norm that is infinite or NaN
  * gives factors of 0 or NaN, as the formulas say.  max_norm or eps negative or
- * NaN: RC_ERR_RANGE; max_norm = INFINITY: the norm alone and the scale.
+ * NaN: RC_ERR_RANGE; max_norm = INFINITY: the norm alone and the scale, whatever
+ * the norm is.
  * workspace: rc_grad_norm_clip_workspace() bytes, 16-byte aligned. */
 typedef struct { const void *in; void *out; uint64_t n; int32_t in_t, out_t; } rc_grad;
 size_t rc_grad_norm_clip_workspace(void);

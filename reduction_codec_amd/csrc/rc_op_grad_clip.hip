@@ -1,7 +1,7 @@
 // Global norm of many tensors, and clipping by it.
 //
 //   N = |scale| sqrt(sum over all tensors of g^2)
-//   out = round(g * scale * min(1, max_norm / (N + eps)))
+//   out = round(g * scale * min(1, max_norm / (N + eps)))   (max_norm infinite: g * scale)
 //
 // Two kernels read the tensors through a table in the kernel arguments (no
 // device copy of the pointers, so a call can be captured and replayed).  Every
@@ -178,7 +178,7 @@ __global__ __launch_bounds__(kThreads) void grad_scale_kernel(const Table t, con
     const float nrm = (float)(sqrt(group_total64(s, slot)) * (double)fabsf(scale));
     if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = nrm;
     float f = max_norm / (nrm + eps);
-    f = (f > 1.0f ? 1.0f : f) * scale;           // a NaN norm stays NaN
+    f = (f > 1.0f || isinf(max_norm) ? 1.0f : f) * scale;   // a NaN norm stays NaN, but no limit clips nothing
     const uint32_t total = t.first[t.count];
     int k = 0;
     for (uint32_t c = blockIdx.x; c < total; c += gridDim.x) {
