@@ -17,10 +17,10 @@
 // expert by a wave-wide scan of the bounds, and a grid for the largest number
 // of tiles that the sizes allow is launched (surplus workgroups end at once).
 // Bounds are clamped to the rows there are, so no bounds can reach outside.
-#include <algorithm>
 #include <type_traits>
 #include "rc_op.hpp"
 #include "rc_op_launch.hpp"
+#include "rc_op_rules.hpp"
 
 namespace rc {
 namespace {
@@ -1071,76 +1071,42 @@ hipError_t launch_dx(const Grouped& a, hipStream_t st)
     return hipGetLastError();
 }
 
-// Forward.  The mean rows of an expert choose how many rows a workgroup takes
-// (the weights are read and decoded once per 16 MF rows, but rows that are not
-// there cost as much as others), the number of workgroups how they are cut.
-// bf16, 32 experts of 2048 x 4096, in us with 16, 32, 64, 128 rows: mean 6: 40,
-// 39, 45, -; mean 16: 51, 51, 55, -; mean 64: 114, 87, 83, 105; mean 128: -, -,
-// 124, 130; mean 256: -, -, 208, 194.  128 x 256 tiles pay once there are
-// several rounds of them: 16384 rows of 8192 x 4096 1110 us -> 1073, but 8192
-// rows of 2048 x 4096 177 -> 192.  With few workgroups more and smaller ones:
-// 600 rows of 1000 x 2080 15 us with 32 rows, 22 with 64; 2331 and 6000 rows 27
-// and 45 with 64 x 256, 30 and 48 with 128 x 128, 33 and 59 with 64 x 128.
-// There two groups of waves with every second span each did not help (2331 rows
-// 27 us either way in bf16, 28 -> 33 in fp16), nor did waves split over rows
-// too, in any tile (16384 rows 1104 -> 1422).
-// Three terms take LDS and registers, so fp32 stays with 32 rows: mean 64 with
-// 32 x 128, 32 x 256, 64 x 256: 160, 145, 174.  Fewer still leave the card
-// idle, and the contraction is cut instead: two rows of 4096 x 4096 take 8 us
-// so, 14 us otherwise; 248 workgroups 9.4 and 8.2 us.
+inline GroupedSizes sizes_of(const Grouped& a) { return {a.rows, (size_t)a.experts, a.n, a.k}; }
+
 template <int DT>
 hipError_t launch_forward(const Grouped& a, hipStream_t st)
 {
-    constexpr int SB = DT == kF32 ? 8 : 16;
-    const size_t mean = (a.rows + a.experts - 1) / a.experts;
-    // workgroups, about, for tiles of so many rows and columns
-    const auto groups = [&](size_t rows, size_t columns) {
-        return std::min(a.rows, a.rows / rows + (size_t)a.experts) * ((a.n + columns - 1) / columns);
-    };
-    if (groups(16, 128) < 192) return launch_thin<DT, 1, 2, 4>(a, st);
-    if (mean <= 8) return launch_slim<DT, 1, 1, 8, SB>(a, st);
-    if constexpr (DT != kF32) {
-        if (mean <= 40) return launch_slim<DT, 2, 1, 8, 16>(a, st);
-        if (groups(64, 128) < 256) return launch_slim<DT, 2, 1, 8, 8>(a, st);
-        if (mean <= 160) return launch_slim<DT, 4, 1, 8, 8>(a, st);
-        if (groups(64, 256) < 768) return launch_slim<DT, 4, 2, 8, 4>(a, st);
-        if (groups(128, 256) < 1024) return launch_slim<DT, 8, 2, 4, 4>(a, st);
-        return launch_slim<DT, 8, 2, 8, 4>(a, st);
-    } else {
-        if (mean <= 40 || groups(64, 256) < 128) return launch_slim<DT, 2, 2, 4, 4>(a, st);
+    const Forward form = forward_form(DT == kF32, sizes_of(a));
+    if (form == Forward::kThin16x32) return launch_thin<DT, 1, 2, 4>(a, st);
+    if (form == Forward::k16x128) return launch_slim<DT, 1, 1, 8, DT == kF32 ? 8 : 16>(a, st);
+    if constexpr (DT == kF32) {
+        if (form == Forward::k32x128F32) return launch_slim<DT, 2, 2, 4, 4>(a, st);
         return launch_slim<DT, 2, 2, 8, 4>(a, st);
+    } else {
+        switch (form) {
+        case Forward::k32x128Span16: return launch_slim<DT, 2, 1, 8, 16>(a, st);
+        case Forward::k32x128Span8: return launch_slim<DT, 2, 1, 8, 8>(a, st);
+        case Forward::k64x128: return launch_slim<DT, 4, 1, 8, 8>(a, st);
+        case Forward::k64x256: return launch_slim<DT, 4, 2, 8, 4>(a, st);
+        case Forward::k128x128: return launch_slim<DT, 8, 2, 4, 4>(a, st);
+        default: return launch_slim<DT, 8, 2, 8, 4>(a, st);
+        }
     }
 }
 
-// Gradients.  dx: 64 x 128 tiles until there are enough of 128 x 256; 16 experts
-// of 2048 x 4096 in bf16, in us: mean 8: 32, 40; mean 64: 45, 53; mean 72: 57,
-// 53; mean 128: 75, 62; mean 256: 125, 99; mean 512: 225, 166; 4282 rows on two
-// experts of 6856 x 256 74, 126; 4096 rows on 8 of 1024 x 1024 (160 large tiles)
-// 23, 25.  Very few: four
-// groups of waves share the contraction, 37 rows of 3624 x 128 37 -> 19 us, 32
-// rows over 4 experts of 1024 x 1024 12.7 -> 8.2, but 138 tiles 74 -> 80.  fp16
-// with 64 x 128 and 128 x 256: mean 64 68, 100; mean 128 120, 123; mean 256 196,
-// 187; mean 512 348, 312.
-// dW, 256 x 256 and 128 x 128: 64 large tiles 18, 10; 128: 34, 22; 320: 30, 25;
-// 640: 51, 57; 2048: 222, 267.
 template <int DIR, int DT>
 hipError_t launch_backward(const Grouped& a, hipStream_t st)
 {
-    const size_t experts = (size_t)a.experts, mean = (a.rows + experts - 1) / experts;
-    // workgroups, about, for dx tiles of so many rows and columns
-    [[maybe_unused]] const auto groups = [&](size_t rows, size_t columns) {
-        return std::min(a.rows, a.rows / rows + experts) * ((a.k + columns - 1) / columns);
-    };
     if constexpr (DIR == kDx) {
-        if (groups(64, 128) < 100) return launch_tile<DIR, DT, 64, 64, 2, 2, 64, DT == kBF16 ? 4 : 2>(a, st);
-        if (mean <= (DT == kBF16 ? 64 : 128) || groups(128, 256) < 256) return launch_tile<DIR, DT, 64, 128, 2, 2>(a, st);
+        const Dx form = dx_form(DT == kBF16, sizes_of(a));
+        if (form == Dx::k64x64Shared) return launch_tile<DIR, DT, 64, 64, 2, 2, 64, DT == kBF16 ? 4 : 2>(a, st);
+        if (form == Dx::k64x128) return launch_tile<DIR, DT, 64, 128, 2, 2>(a, st);
         if constexpr (DT == kBF16) return launch_dx(a, st);
         else return launch_tile<DIR, DT, 128, 256, 2, 4>(a, st);
     } else if constexpr (DT == kF32) {
         return launch_tile<DIR, DT, 128, 128, 2, 4, 32>(a, st);
     } else {
-        if ((size_t)((a.n + 255) / 256) * ((a.k + 255) / 256) * experts < 512) return launch_dw<DT == kF16, 128>(a, st);
-        return launch_dw<DT == kF16, 256>(a, st);
+        return dw_form(false, sizes_of(a)) == Dw::k128x128 ? launch_dw<DT == kF16, 128>(a, st) : launch_dw<DT == kF16, 256>(a, st);
     }
 }
 
