@@ -230,10 +230,16 @@ rc_status rc_copy(const void *in, void *out, size_t bytes, void *stream);
  * no access outside the buffers.
  * k must be a multiple of 32 (an MXFP4 block does not cross rows) and n one of
  * 8, both at most RC_MAX_WIDTH, rows below 2^31, experts at most
- * RC_MAX_EXPERTS, else RC_ERR_RANGE.  Products are exact and sums FP32 (the
- * order is fixed by sizes and offsets, so calls repeat bit for bit): each sum
- * s of N products p satisfies |s - sum p| <= (N + 3) 2^-23 sum |p|.  With fp16
- * and fp32 rows an infinity may come out as NaN. */
+ * RC_MAX_EXPERTS, else RC_ERR_RANGE.  Sums are FP32 (the order is fixed by
+ * sizes and offsets, so calls repeat bit for bit) and products exact, but for
+ * dW of fp32 rows, where each is formed to within 2^-22 of itself (six of the
+ * nine products of two values' three bfloat16 terms).  Each sum s of N products
+ * p satisfies |s - sum p| <= (N + 3) 2^-23 sum |p|, where fp32 rows' values
+ * count as the nearest multiple of 2^-133.  What is not finite stays in its row
+ * (in dW: its group's row or column) and everything there that the formulas
+ * make infinite or NaN is not finite; with fp32 rows, and with fp16 rows but in
+ * dW, an infinity may come out as NaN, as sizes and its own expert's weights
+ * have it. */
 rc_status rc_mxfp4_grouped_matmul(const void *w, size_t experts, size_t n, size_t k, const int32_t *offsets,
                                   rc_dtype x_t, const void *x, size_t rows, rc_dtype y_t, void *y, void *stream);
 rc_status rc_mxfp4_grouped_matmul_dx(const void *w, size_t experts, size_t n, size_t k, const int32_t *offsets,
