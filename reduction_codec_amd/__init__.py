@@ -95,6 +95,20 @@ def lib() -> ctypes.CDLL:
         raise RuntimeError(f"{LIB_PATH} is not built; run `python -c 'import __graft_entry__ as g; g.build()'` "
                            "(the codec has no CPU fallback)")
     l = ctypes.CDLL(LIB_PATH)
+    try:
+        l.rc_abi_version.restype, l.rc_abi_version.argtypes = ctypes.c_int, []
+        if l.rc_abi_version() != ABI_VERSION:
+            raise RuntimeError(f"{LIB_PATH} has ABI version {l.rc_abi_version()}, this binding expects "
+                               f"{ABI_VERSION}; rebuild the library")
+        _declare(l)
+    except AttributeError as e:                          # functions are added without a new version
+        raise RuntimeError(f"{LIB_PATH} is older than this binding ({e}); rebuild the library") from None
+    _lib = l
+    return l
+
+
+def _declare(l: ctypes.CDLL):
+    """The types of the library's functions."""
     vp, sz, i32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
     l.rc_tile_bytes.restype, l.rc_tile_bytes.argtypes = sz, [Codec]
     l.rc_packed_bytes.restype, l.rc_packed_bytes.argtypes = sz, [Codec, sz]
@@ -123,12 +137,6 @@ def lib() -> ctypes.CDLL:
     l.rc_grad_norm_clip_workspace.restype, l.rc_grad_norm_clip_workspace.argtypes = sz, []
     l.rc_grad_norm_clip.restype, l.rc_grad_norm_clip.argtypes = i32, [vp, sz, f32, f32, f32, vp, vp, vp]
     l.rc_status_str.restype, l.rc_status_str.argtypes = ctypes.c_char_p, [i32]
-    l.rc_abi_version.restype, l.rc_abi_version.argtypes = i32, []
-    if l.rc_abi_version() != ABI_VERSION:
-        raise RuntimeError(f"{LIB_PATH} has ABI version {l.rc_abi_version()}, this binding expects "
-                           f"{ABI_VERSION}; rebuild the library")
-    _lib = l
-    return l
 
 
 def _codec(c) -> Codec:
