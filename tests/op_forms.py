@@ -76,6 +76,8 @@ SHAPES = [
     # gradients: several column tiles with a partial last one, 0 to 4 steps after the four-step loop
     (ragged(8, 200), 520, 3296), (ragged(8, 200), 552, 3296), (ragged(8, 200), 584, 3296), (ragged(8, 200), 616, 3296),
     (ragged(8, 200), 640, 3328), (ragged(8, 200), 1032, 3296), (ragged(8, 130), 1088, 3328),
+    # more experts than one scan of the bounds takes
+    (ragged(200, 70), 264, 544), (ragged(130, 3), 264, 288),
 ]
 
 

@@ -138,3 +138,36 @@ def test_blocks_freed_by_queued_work_are_left_alone():
     torch.cuda.synchronize()
     assert all(torch.equal(u, v) for u, v in zip(got, want))
     assert (sink == 24.0).all()
+
+
+@pytest.mark.gpu
+def test_another_stream_inside_a_captured_graph():
+    """A graph that forks to a second stream, whose outputs come from that stream's memory: replays with new inputs, with
+    eager work on freed blocks in between, equal the eager results."""
+    dev = torch.device("cuda:0")
+    g = torch.Generator(device=dev).manual_seed(1)
+    rn = lambda *s: torch.randn(*s, generator=g, device=dev).to(torch.bfloat16)  # noqa: E731
+    y, r, pre = rn(300, 520), rn(300, 520), rn(520)
+
+    def run(stream):
+        h, z, st = rca.block_norm(y, r, pre, post_weight=pre, stats=True, stream=stream)
+        return [h, z, *rca.block_norm_backward(z, h, h, st, y, pre, post_weight=pre, stream=stream)[:4]]
+
+    main, side = torch.cuda.Stream(device=dev), torch.cuda.Stream(device=dev)
+    run(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        side.wait_stream(main)
+        first = run(side)
+        second = run(None)                                 # on the capturing stream, beside the other
+        main.wait_stream(side)
+    for _ in range(4):
+        y.copy_(rn(300, 520))
+        r.copy_(rn(300, 520))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = run(None)
+        for got in (first, second):
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+        torch.cuda.synchronize()
