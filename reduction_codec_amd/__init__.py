@@ -390,7 +390,7 @@ def _check_on(t: torch.Tensor, name: str, index: int):
 def _result(out, shape, dtype, dev: torch.device, stream, name: str) -> torch.Tensor:
     """The caller's output, checked, or a new one for work on `stream`."""
     if out is None:
-        return _new(shape, dtype, dev, stream)
+        return torch.empty(shape, dtype=dtype, device=dev) if stream is None else _new(shape, dtype, dev, stream)
     _check_on(out, name, dev.index)
     if out.dtype != dtype or tuple(out.shape) != tuple(shape):
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
