@@ -13,13 +13,18 @@
 // All of it in binary32, every output rounded once.  The work is memory-bound:
 // 4 (forward) or 6 (backward) elements per value of a row, so each element is
 // read once into registers, a workgroup holds a whole row, and only the two
-// row sums go through LDS.
+// row sums go through LDS.  1024 lanes have 128 registers each, which rows wider
+// than 16384 forward, and than 8192 backward, overrun: the compiler keeps the
+// rest in scratch memory (160 to 430 bytes a lane forward; backward 220 to 490
+// up to a width of 16384, 970 to 1490 beyond), which costs time.
 //
 // bf16, forward: 16384 x 8192 197 us (1.07 GB, 5.4 TB/s), 16384 x 4096 100, one
 // row of 4096 3.6; with the next row's loads ahead 211 and 104, with 32 elements
 // per lane 208 and 117, with 4096 lanes per unit 200 and 105.  Backward: 8192 x
 // 4096 91 us (403 MB and 34 of column sums), 8192 x 8192 161, 16384 x 1024 52;
-// fp32 with a full gate 2500 x 1999 49, 2500 x 2000 38.
+// fp32 with a full gate 2500 x 1999 49, 2500 x 2000 38.  Wide rows: forward 8192 x
+// 16384 202, 2048 x 32768 150 (537 MB); backward 4096 x 8192 92, 4096 x 16384 392
+// (805 MB both this and the next), 2048 x 32768 1090.
 #include "rc_op.hpp"
 #include "rc_op_launch.hpp"
 

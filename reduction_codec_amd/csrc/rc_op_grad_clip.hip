@@ -15,8 +15,8 @@
 // chunks from the last to the first, so that what the first kernel read last
 // is still in the 256 MiB cache; its stores do not go there.
 //
-// Bound by memory: two reads and a write.  805 M bf16 values into others 876 us
-// (4.8 GB, 5.5 TB/s), 33 M fp16 values in 104 tensors at odd places 40 us, 1.8 M
+// Bound by memory: two reads and a write.  805 M bf16 values into others 876 -
+// 892 us (4.8 GB, 5.4 - 5.5 TB/s), in place 744, 30 M fp16 values in 104 tensors at odd places 40 us, 1.8 M
 // fp32 in 48 tensors 10.5 us, of which half are the two launches.  Measured
 // against: 2048 workgroups 901 us, 8 or 2 loads per lane 909, 923, cached
 // stores 902, uncached loads in the second pass 852 but 42 and 11.4 us for the
