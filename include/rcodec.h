@@ -296,6 +296,89 @@ size_t rc_grad_norm_clip_workspace(void);
 rc_status rc_grad_norm_clip(const rc_grad *grads, size_t count, float scale, float max_norm, float eps,
                             void *workspace, float *norm, void *stream);
 
+/* ---- A paged cache of keys and values in MXFP4 ---------------------------------
+ *
+ * What attention reads before a tensor-parallel block's first all-reduce, held in
+ * the codec's tiles: a page has room for `page` tokens, and what it holds of one
+ * head is a packed stream {MXFP4, E8M0, 32} of page * d values, token by token
+ * (rc_quantize_pack and rc_unpack_dequant read and write such streams).  k and v
+ * are pages x kv_heads of these streams each, one after another.
+ * Sequence s has lengths[s] tokens in the cache, the new ones among them; token j
+ * is in page table[s * max_pages + j / page], at place j % page.  Rows
+ * offsets[s] <= i < offsets[s + 1] of what a call takes are the sequence's last
+ * tokens: row i stands at position lengths[s] - offsets[s + 1] + i.
+ * table, lengths and offsets are device arrays, read by the kernels (a captured
+ * graph follows them), and what they hold cannot lead outside the buffers:
+ * lengths count as at least 0 and at most max_pages * page, offsets are clamped to
+ * the rows there are, and pages outside [0, pages) hold no token.
+ * Offsets that do not ascend give unspecified results.  Rows that belong to no
+ * sequence (before offsets[0], from offsets[seqs] on) are neither read nor written.
+ * d is 64, 96, 128, 192 or 256; page a power of two from 16 to 65536 with page * d
+ * a multiple of 2048; kv_heads and seqs at most 65535; pages, tokens and
+ * max_pages * page below 2^31; else RC_ERR_RANGE.  No alignment beyond their
+ * elements' is asked of table, lengths and offsets. */
+#define RC_MAX_SEQS 65535
+typedef struct {
+    void *k, *v;
+    uint64_t pages, page, kv_heads, d;
+    const int32_t *table;
+    uint64_t seqs, max_pages;
+    const int32_t *lengths, *offsets;
+} rc_cache;
+
+/* Write the new tokens' keys and values (tokens x kv_heads x d, of type t) to the
+ * cache, each key turned by its position on the way, and turn the queries q
+ * (tokens x heads x d) into q_out: for the pairs (a, b) of the first `rot` values
+ * of a head, (i, i + rot/2), or (2i, 2i + 1) if `interleaved`, i < rot/2,
+ *   a' = a cos - b sin,  b' = b cos + a sin
+ * with cos = rotation[p][i], sin = rotation[p][rot/2 + i] for position p.  The
+ * turned values are formed in binary64; q_out is rounded once, and codes and scales
+ * are those that the codec's rule gives for the turned values themselves (for what
+ * is not turned: the bytes that rc_quantize_pack writes).
+ * Rows of k, v and q are k_stride, v_stride and q_stride elements apart (a fused
+ * projection's parts are taken where they lie), multiples of 16 bytes, at least a
+ * row's length and at most 2^31 bytes; q_out is dense.  rotation: `positions` >=
+ * max_pages * page rows of `rot` values, NULL or rot = 0 for none; rot is a
+ * multiple of 16, at most d.  heads is a multiple of kv_heads, at most 65535, or 0
+ * without q.  A token whose position is negative or whose page does not exist is
+ * not written to the cache; its query is turned by position 0 if the position is
+ * negative.  Two rows on one place of the cache: unspecified which, or which parts,
+ * of them it holds.  q_out == q: RC_ERR_UNSUPPORTED
+ * (no overlap).  NaN and infinity: codes unspecified, as everywhere. */
+rc_status rc_mxfp4_cache_append(const rc_cache *cache, rc_dtype t, size_t tokens, const void *k, size_t k_stride,
+                                const void *v, size_t v_stride, size_t heads, const void *q, size_t q_stride,
+                                void *q_out, const float *rotation, size_t positions, size_t rot, int interleaved,
+                                void *stream);
+
+/* The rows' keys and values as the cache holds them (codes times scales, rounded to
+ * t), dense, tokens x kv_heads x d each; rows whose position is negative or whose
+ * page does not exist become zeros. */
+rc_status rc_mxfp4_cache_read(const rc_cache *cache, size_t tokens, rc_dtype t, void *k, void *v, void *stream);
+
+/* Attention of the rows of q (tokens x heads x d of type t, rows q_stride elements
+ * apart as above) over their sequences' tokens in the cache; head h reads head
+ * h / (heads / kv_heads) of it:
+ *   s_j = scale q . K_j,  out = sum_j exp(s_j) V_j / sum_j exp(s_j),
+ *   lse = log sum_j exp(s_j)
+ * over the tokens j that the row sees: those that are there (a length and a page
+ * tell), and if `causal` j <= p, the row's own position, and if window > 0 (causal
+ * only, else RC_ERR_UNSUPPORTED) j > p - window.  out: dense, of type t; lse:
+ * tokens x heads fp32 values, or NULL.  A row that sees nothing, or only scores of
+ * minus infinity, gets out = 0 and lse = -infinity.  What the cache holds where a
+ * row does not see does not reach the row, whatever its bytes are; what is not
+ * finite where it sees makes its values not finite.
+ * Scores and sums are FP32.  Rounding: the weights exp(s_j - max) are multiplied as
+ * bfloat16 (t bf16, relative 2^-9), or as two (fp16) or three (fp32) terms of it
+ * that hold 16 and 24 bits, and below 2^-126 may count as zero; fp32 queries count as the nearest multiple of 2^-133.
+ * max_query: no sequence has more rows than this, 0 if not known: a hint that the
+ * choice of kernels goes by, results are right whatever it says.
+ * workspace: rc_mxfp4_cache_attention_workspace(heads, d) bytes, 16-byte aligned,
+ * written before it is read, for one call at a time.  Calls repeat bit for bit. */
+size_t rc_mxfp4_cache_attention_workspace(size_t tokens, size_t heads, size_t kv_heads, size_t d);
+rc_status rc_mxfp4_cache_attention(const rc_cache *cache, rc_dtype t, size_t tokens, size_t heads, const void *q,
+                                   size_t q_stride, float scale, int causal, size_t window, size_t max_query,
+                                   void *out, float *lse, void *workspace, void *stream);
+
 /* Static description of a status code; never NULL. */
 const char *rc_status_str(rc_status s);
 

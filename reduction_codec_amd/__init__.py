@@ -20,6 +20,16 @@ and the operators around a quantized all-reduce:
 * ``block_norm(y, residual, pre_weight, ...)``, ``block_norm_backward``
                                            -> norms around a block, gate, residual
 * ``grad_norm_clip(grads, max_norm)``  -> global norm of many tensors, clipping
+
+and a paged cache of keys and values held in MXFP4:
+
+* ``mxfp4_cache_new(pages, kv_heads, page, d, device)`` -> (k_cache, v_cache)
+* ``mxfp4_cache_append(k, v, k_cache, v_cache, table, lengths, offsets, q=...)``
+                                           -> q turned by its positions, or None
+* ``mxfp4_cache_attention(q, k_cache, v_cache, table, lengths, offsets)``
+                                           -> out, or (out, log-sum-exp)
+* ``mxfp4_cache_read(k_cache, v_cache, table, lengths, offsets, tokens, d)``
+                                           -> (k, v) as the cache holds them
 """
 from __future__ import annotations
 
@@ -136,6 +146,13 @@ def _declare(l: ctypes.CDLL):
                                          vp, vp, vp, vp, vp, vp, vp]
     l.rc_grad_norm_clip_workspace.restype, l.rc_grad_norm_clip_workspace.argtypes = sz, []
     l.rc_grad_norm_clip.restype, l.rc_grad_norm_clip.argtypes = i32, [vp, sz, f32, f32, f32, vp, vp, vp]
+    l.rc_mxfp4_cache_append.restype = i32
+    l.rc_mxfp4_cache_append.argtypes = [vp, i32, sz, vp, sz, vp, sz, sz, vp, sz, vp, vp, sz, sz, i32, vp]
+    l.rc_mxfp4_cache_read.restype, l.rc_mxfp4_cache_read.argtypes = i32, [vp, sz, i32, vp, vp, vp]
+    l.rc_mxfp4_cache_attention_workspace.restype = sz
+    l.rc_mxfp4_cache_attention_workspace.argtypes = [sz, sz, sz, sz]
+    l.rc_mxfp4_cache_attention.restype = i32
+    l.rc_mxfp4_cache_attention.argtypes = [vp, i32, sz, sz, vp, sz, f32, i32, sz, sz, vp, vp, vp, vp]
     l.rc_status_str.restype, l.rc_status_str.argtypes = ctypes.c_char_p, [i32]
 
 
@@ -628,3 +645,138 @@ def grad_norm_clip(grads, max_norm: float, scale: float = 1.0, eps: float = 1e-6
     _launch("rc_grad_norm_clip", dev, stream, desc.buffer_info()[0], len(grads), scale, max_norm, eps, ws.data_ptr(),
             norm.data_ptr())
     return norm
+
+
+# ------------------------------------------------- a paged cache in MXFP4 ----
+
+def mxfp4_cache_new(pages: int, kv_heads: int, page: int, d: int, device):
+    """(k_cache, v_cache) with room for `pages` pages of `page` tokens, all
+    zeros: uint8 tensors pages x kv_heads x bytes, where the last dimension is
+    the packed stream {MXFP4, E8M0, 32} of one head's page * d values."""
+    if page * d % TILE != 0:
+        raise ValueError("page * d must be a multiple of 2048")
+    shape = (pages, kv_heads, page * d // TILE * MXFP4_TILE_BYTES)
+    return torch.zeros(shape, dtype=torch.uint8, device=device), torch.zeros(shape, dtype=torch.uint8, device=device)
+
+
+def _cache(k_cache, v_cache, table, lengths, offsets, d: int) -> array.array:
+    """rc_cache of checked tensors, as its eleven 64-bit words."""
+    _check_dev(k_cache, "k_cache")
+    index = k_cache.get_device()
+    for name, t in (("v_cache", v_cache), ("table", table), ("lengths", lengths), ("offsets", offsets)):
+        _check_on(t, name, index)
+    shape = k_cache.shape
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8 or len(shape) != 3 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must be uint8 tensors of one shape, pages x kv_heads x bytes")
+    if d <= 0 or shape[2] % MXFP4_TILE_BYTES or shape[2] // MXFP4_TILE_BYTES * TILE % d:
+        raise ValueError("a page of one head must be whole MXFP4 tiles of whole rows of d values")
+    if table.dtype != torch.int32 or lengths.dtype != torch.int32 or offsets.dtype != torch.int32:
+        raise ValueError("table, lengths and offsets must be int32 tensors")
+    seqs = lengths.numel()
+    if lengths.dim() != 1 or offsets.dim() != 1 or offsets.numel() != seqs + 1 or table.dim() != 2 or \
+            table.shape[0] != seqs:
+        raise ValueError("need table (sequences x pages), lengths (sequences) and offsets (sequences + 1)")
+    return array.array("Q", (k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[2] // MXFP4_TILE_BYTES * TILE // d,
+                             shape[1], d, table.data_ptr(), seqs, table.shape[1], lengths.data_ptr(),
+                             offsets.data_ptr()))
+
+
+def _head_rows(t: torch.Tensor, name: str, index: int):
+    """(tokens, heads, d, elements from a token to the next) of a tensor whose
+    tokens' rows are dense; tokens may lie apart, as parts of a wider tensor do."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions, tokens, heads and values")
+    tokens, heads, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and heads > 1):
+        raise ValueError(f"the heads of a token of {name} must lie one after another")
+    return tokens, heads, d, s0 if tokens > 1 else heads * d
+
+
+def mxfp4_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       table: torch.Tensor, lengths: torch.Tensor, offsets: torch.Tensor,
+                       q: torch.Tensor | None = None, rotation: torch.Tensor | None = None,
+                       interleaved: bool = False, q_out: torch.Tensor | None = None, stream=None):
+    """Write new tokens' keys and values (tokens x kv_heads x d) to the cache,
+    keys turned by their positions, and return the queries (tokens x heads x d)
+    turned alike, or None without q.  Rows offsets[s] to offsets[s + 1] are the
+    last tokens of sequence s, which has lengths[s] with them; token j of it is
+    in page table[s, j // page].  rotation: fp32, at least table.shape[1] * page
+    rows of the cosines, then the sines of a position's angles:
+
+        angle = position[:, None] * base ** (-torch.arange(r // 2) / (r // 2))  # in float64
+        rotation = torch.cat([angle.cos(), angle.sin()], 1).float()             # positions x r
+
+    turning pairs (i, i + r/2) of the first r values of a head, or (2i, 2i + 1)
+    if `interleaved`.  k, v and q may be parts of one wider tensor.  See
+    rc_mxfp4_cache_append."""
+    _check_dev(k_cache, "k_cache")
+    dev, index = k_cache.device, k_cache.get_device()
+    tokens, kv_heads, d, k_stride = _head_rows(k, "k", index)
+    vt, vh, vd, v_stride = _head_rows(v, "v", index)
+    cache = _cache(k_cache, v_cache, table, lengths, offsets, d)
+    if (vt, vh, vd) != (tokens, kv_heads, d) or v.dtype != k.dtype or kv_heads != k_cache.shape[1]:
+        raise ValueError("k and v must have one shape and dtype, and the cache's heads")
+    t, heads, q_stride, positions, rot = _dtype(k.dtype, "k"), 0, 0, 0, 0
+    if rotation is not None:
+        _check_on(rotation, "rotation", index)
+        if rotation.dtype != torch.float32 or rotation.dim() != 2:
+            raise ValueError("rotation must be a float32 tensor, positions x values")
+        positions, rot = rotation.shape
+    if q is not None:
+        qt, heads, qd, q_stride = _head_rows(q, "q", index)
+        if (qt, qd) != (tokens, d) or q.dtype != k.dtype:
+            raise ValueError("q must have k's tokens, width and dtype")
+        q_out = _result(q_out, (tokens, heads, d), q.dtype, dev, stream, "q_out")
+    _launch("rc_mxfp4_cache_append", dev, stream, cache.buffer_info()[0], t, tokens, k.data_ptr(), k_stride,
+            v.data_ptr(), v_stride, heads, _ptr(q), q_stride, None if q is None else q_out.data_ptr(),
+            _ptr(rotation), positions, rot, int(interleaved))
+    return None if q is None else q_out
+
+
+def mxfp4_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
+                     offsets: torch.Tensor, tokens: int, d: int, dtype: torch.dtype = torch.bfloat16,
+                     k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+    """(k, v), tokens x kv_heads x d each: the rows' keys and values as the
+    cache holds them, decoded; rows offsets[s] to offsets[s + 1] are the last
+    tokens of sequence s (all of them if offsets are the lengths' sums).  See
+    rc_mxfp4_cache_read."""
+    cache = _cache(k_cache, v_cache, table, lengths, offsets, d)
+    dev = k_cache.device
+    t, shape = _dtype(dtype, "output"), (tokens, k_cache.shape[1], d)
+    k, v = _result(k, shape, dtype, dev, stream, "k"), _result(v, shape, dtype, dev, stream, "v")
+    _launch("rc_mxfp4_cache_read", dev, stream, cache.buffer_info()[0], tokens, t, k.data_ptr(), v.data_ptr())
+    return k, v
+
+
+def mxfp4_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
+                          lengths: torch.Tensor, offsets: torch.Tensor, scale: float | None = None,
+                          causal: bool = True, window: int = 0, max_query: int | None = None, lse: bool = False,
+                          out: torch.Tensor | None = None, stream=None):
+    """Attention of the queries (tokens x heads x d, heads a multiple of the
+    cache's) over their sequences' tokens in the cache, the new ones included:
+    rows offsets[s] to offsets[s + 1] stand at the last positions of sequence
+    s, and see what is at or before them (`causal`), the last `window` of that
+    if window > 0.  scale: 1 / sqrt(d) by default.  max_query: the most rows a
+    sequence has, if known (it only helps to choose the kernel).  Returns out
+    (like q, dense), or (out, the fp32 log-sum-exp of tokens x heads).  See
+    rc_mxfp4_cache_attention."""
+    _check_dev(k_cache, "k_cache")
+    dev = k_cache.device
+    tokens, heads, d, q_stride = _head_rows(q, "q", k_cache.get_device())
+    cache = _cache(k_cache, v_cache, table, lengths, offsets, d)
+    if window < 0 or (max_query is not None and max_query < 0):
+        raise ValueError("window and max_query must not be negative")
+    t = _dtype(q.dtype, "q")
+    out = _result(out, (tokens, heads, d), q.dtype, dev, stream, "out")
+    sums = _result(None, (tokens, heads), torch.float32, dev, stream, "") if lse else None
+    ws = _result(None, ((_lib or lib()).rc_mxfp4_cache_attention_workspace(tokens, heads, k_cache.shape[1], d),),
+                 torch.uint8, dev, stream, "")
+    _launch("rc_mxfp4_cache_attention", dev, stream, cache.buffer_info()[0], t, tokens, heads, q.data_ptr(), q_stride,
+            d ** -0.5 if scale is None else scale, int(causal), window, max_query or 0, out.data_ptr(), _ptr(sums),
+            ws.data_ptr())
+    return (out, sums) if lse else out

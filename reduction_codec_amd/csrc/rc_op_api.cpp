@@ -25,6 +25,39 @@ rc_status grouped_sizes(size_t experts, size_t n, size_t k, size_t rows)
     return RC_OK;
 }
 
+// A cache's sizes; RC_OK when the kernels can address it.
+rc_status cache_sizes(const rc_cache& c, size_t tokens)
+{
+    const uint64_t d = c.d, p = c.page;
+    if (d != 64 && d != 96 && d != 128 && d != 192 && d != 256) return RC_ERR_RANGE;
+    if (p < 16 || p > 65536 || (p & (p - 1)) != 0 || p * d % RC_TILE_ELEMS != 0) return RC_ERR_RANGE;
+    if (c.kv_heads < 1 || c.kv_heads > 65535 || c.seqs > RC_MAX_SEQS || c.pages > 0x7FFFFFFF || tokens > 0x7FFFFFFF ||
+        c.max_pages > 0x7FFFFFFF / p) return RC_ERR_RANGE;
+    if (p * d > kMaxElems / c.kv_heads || (c.pages != 0 && p * d * c.kv_heads > kMaxElems / c.pages)) return RC_ERR_RANGE;
+    return RC_OK;
+}
+
+rc_status cache_pointers(const rc_cache& c)
+{
+    if (!c.offsets || !c.lengths || (c.max_pages != 0 && !c.table) || (c.pages != 0 && (!c.k || !c.v))) return RC_ERR_NULL;
+    if (!aligned16(c.k) || !aligned16(c.v) || !aligned(c.table, 4) || !aligned(c.lengths, 4) || !aligned(c.offsets, 4)) return RC_ERR_ALIGN;
+    return RC_OK;
+}
+
+rc::Cache cache_args(const rc_cache& c, size_t tokens)
+{
+    int shift = 0;
+    while ((1u << shift) < c.page) ++shift;
+    return {static_cast<uint8_t*>(c.k), static_cast<uint8_t*>(c.v), c.table, c.lengths, c.offsets, (int)c.pages, shift,
+            (int)c.kv_heads, (int)c.seqs, (int)c.max_pages, (int)tokens, (uint32_t)(c.page * c.d / RC_TILE_ELEMS * 1088)};
+}
+
+// Rows of `width` elements, `stride` apart.
+bool stride_ok(size_t stride, size_t width, int t)
+{
+    return stride >= width && stride <= ((size_t)1 << 31) / dtype_size(t) && stride * dtype_size(t) % 16 == 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -126,6 +159,69 @@ rc_status rc_grad_norm_clip(const rc_grad* grads, size_t count, float scale, flo
     static_assert(sizeof(rc_grad) == sizeof(rc::GradTensor), "one layout");
     return from_hip(rc::launch_grad_norm_clip(reinterpret_cast<const rc::GradTensor*>(grads), count, scale, max_norm,
                                               eps, workspace, norm, static_cast<hipStream_t>(stream)));
+}
+
+rc_status rc_mxfp4_cache_append(const rc_cache* cache, rc_dtype t, size_t tokens, const void* k, size_t k_stride,
+                                const void* v, size_t v_stride, size_t heads, const void* q, size_t q_stride,
+                                void* q_out, const float* rotation, size_t positions, size_t rot, int interleaved,
+                                void* stream)
+{
+    if (!cache) return RC_ERR_NULL;
+    if (!dtype_ok(t)) return RC_ERR_UNSUPPORTED;
+    const rc_status s = cache_sizes(*cache, tokens);
+    if (s != RC_OK) return s;
+    const size_t d = cache->d, kv = cache->kv_heads;
+    if (heads > 65535 || heads % kv != 0 || rot % 16 != 0 || rot > d) return RC_ERR_RANGE;
+    if (rotation && rot != 0 && positions < cache->max_pages * cache->page) return RC_ERR_RANGE;
+    if (tokens == 0 || cache->seqs == 0) return RC_OK;
+    if (!stride_ok(k_stride, kv * d, t) || !stride_ok(v_stride, kv * d, t) || (heads != 0 && !stride_ok(q_stride, heads * d, t))) return RC_ERR_RANGE;
+    if (q_out == q && q != nullptr && heads != 0) return RC_ERR_UNSUPPORTED;
+    if (!k || !v || (heads != 0 && (!q || !q_out))) return RC_ERR_NULL;
+    const rc_status ps = cache_pointers(*cache);
+    if (ps != RC_OK) return ps;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) || !aligned16(rotation)) return RC_ERR_ALIGN;
+    const rc::CacheAppend a = {cache_args(*cache, tokens), k, v, q, q_out, rot != 0 ? rotation : nullptr, k_stride,
+                               v_stride, q_stride, (int)heads, rotation ? (int)rot : 0, interleaved != 0};
+    return from_hip(rc::launch_cache_append(t, (int)d, a, static_cast<hipStream_t>(stream)));
+}
+
+rc_status rc_mxfp4_cache_read(const rc_cache* cache, size_t tokens, rc_dtype t, void* k, void* v, void* stream)
+{
+    if (!cache) return RC_ERR_NULL;
+    if (!dtype_ok(t)) return RC_ERR_UNSUPPORTED;
+    rc_status s = cache_sizes(*cache, tokens);
+    if (s != RC_OK || tokens == 0 || cache->seqs == 0) return s;
+    if (!k || !v) return RC_ERR_NULL;
+    s = cache_pointers(*cache);
+    if (s != RC_OK) return s;
+    if (!aligned16(k) || !aligned16(v)) return RC_ERR_ALIGN;
+    return from_hip(rc::launch_cache_read(t, (int)cache->d, cache_args(*cache, tokens), k, v, static_cast<hipStream_t>(stream)));
+}
+
+size_t rc_mxfp4_cache_attention_workspace(size_t tokens, size_t heads, size_t kv_heads, size_t d)
+{
+    if (kv_heads == 0 || heads > 65535 || heads % kv_heads != 0 || d > 256) return 0;
+    return rc::cache_attention_work(tokens, heads, kv_heads, d);
+}
+
+rc_status rc_mxfp4_cache_attention(const rc_cache* cache, rc_dtype t, size_t tokens, size_t heads, const void* q,
+                                   size_t q_stride, float scale, int causal, size_t window, size_t max_query,
+                                   void* out, float* lse, void* workspace, void* stream)
+{
+    if (!cache) return RC_ERR_NULL;
+    if (!dtype_ok(t) || (window != 0 && !causal)) return RC_ERR_UNSUPPORTED;
+    rc_status s = cache_sizes(*cache, tokens);
+    if (s != RC_OK) return s;
+    if (heads == 0 || heads > 65535 || heads % cache->kv_heads != 0 || tokens > 0x7FFFFFFF / heads) return RC_ERR_RANGE;
+    if (tokens == 0 || cache->seqs == 0) return RC_OK;
+    if (!stride_ok(q_stride, heads * cache->d, t)) return RC_ERR_RANGE;
+    if (!q || !out || !workspace) return RC_ERR_NULL;
+    s = cache_pointers(*cache);
+    if (s != RC_OK) return s;
+    if (!aligned16(q) || !aligned16(out) || !aligned(lse, 4) || !aligned16(workspace)) return RC_ERR_ALIGN;
+    const rc::CacheAttention a = {cache_args(*cache, tokens), q, out, lse, static_cast<float*>(workspace), q_stride,
+                                  (int)heads, window > 0x7FFFFFFF ? 0 : (int)window, causal != 0, scale};
+    return from_hip(rc::launch_cache_attention(t, (int)cache->d, a, max_query, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -77,4 +77,34 @@ hipError_t launch_grouped_forward(int dt, const Grouped& a, hipStream_t st);
 hipError_t launch_grouped_dx(int dt, const Grouped& a, hipStream_t st);
 hipError_t launch_grouped_dw(int dt, const Grouped& a, hipStream_t st);
 
+// ---- a paged cache in MXFP4 (rc_op_cache.hip, rc_op_attention.hip)
+// rc_cache as the kernels take it.  `shift`: log2 of the page's tokens.
+struct Cache {
+    uint8_t *k, *v;
+    const int32_t *table, *lengths, *offsets;
+    int pages, shift, kv_heads, seqs, max_pages, tokens;
+    uint32_t head_bytes;                         // of one head's stream in a page
+};
+struct CacheAppend {
+    Cache c;
+    const void *k, *v, *q;
+    void* q_out;
+    const float* rotation;
+    size_t k_stride, v_stride, q_stride;
+    int heads, rot, interleaved;
+};
+struct CacheAttention {
+    Cache c;
+    const void* q;
+    void* out;
+    float *lse, *work;
+    size_t q_stride;
+    int heads, window, causal;
+    float scale;
+};
+hipError_t launch_cache_append(int dt, int d, const CacheAppend& a, hipStream_t st);
+hipError_t launch_cache_read(int dt, int d, const Cache& c, void* k, void* v, hipStream_t st);
+size_t cache_attention_work(size_t tokens, size_t heads, size_t kv_heads, size_t d);
+hipError_t launch_cache_attention(int dt, int d, const CacheAttention& a, size_t max_query, hipStream_t st);
+
 }  // namespace rc
