@@ -314,8 +314,8 @@ rc_status rc_grad_norm_clip(const rc_grad *grads, size_t count, float scale, flo
  * Offsets that do not ascend give unspecified results.  Rows that belong to no
  * sequence (before offsets[0], from offsets[seqs] on) are neither read nor written.
  * d is 64, 96, 128, 192 or 256; page a power of two from 16 to 65536 with page * d
- * a multiple of 2048; kv_heads and seqs at most 65535; pages, tokens and
- * max_pages * page below 2^31; else RC_ERR_RANGE.  No alignment beyond their
+ * a multiple of 2048; kv_heads and seqs at most 65535; pages and tokens
+ * below 2^31, max_pages * page at most 2^30; else RC_ERR_RANGE.  No alignment beyond their
  * elements' is asked of table, lengths and offsets. */
 #define RC_MAX_SEQS 65535
 typedef struct {

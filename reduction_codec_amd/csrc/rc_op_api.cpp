@@ -32,7 +32,7 @@ rc_status cache_sizes(const rc_cache& c, size_t tokens)
     if (d != 64 && d != 96 && d != 128 && d != 192 && d != 256) return RC_ERR_RANGE;
     if (p < 16 || p > 65536 || (p & (p - 1)) != 0 || p * d % RC_TILE_ELEMS != 0) return RC_ERR_RANGE;
     if (c.kv_heads < 1 || c.kv_heads > 65535 || c.seqs > RC_MAX_SEQS || c.pages > 0x7FFFFFFF || tokens > 0x7FFFFFFF ||
-        c.max_pages > 0x7FFFFFFF / p) return RC_ERR_RANGE;
+        c.max_pages > ((uint64_t)1 << 30) / p) return RC_ERR_RANGE;
     if (p * d > kMaxElems / c.kv_heads || (c.pages != 0 && p * d * c.kv_heads > kMaxElems / c.pages)) return RC_ERR_RANGE;
     return RC_OK;
 }

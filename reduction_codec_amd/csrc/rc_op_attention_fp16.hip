@@ -1,0 +1,9 @@
+// Attention over a paged cache in MXFP4: the kernels for fp16 queries.
+#include "rc_op_attention.hpp"
+
+namespace rc {
+hipError_t launch_attention_fp16(int d, const CacheAttention& a, size_t most_rows, hipStream_t st)
+{
+    return attention_t<kF16>(d, a, most_rows, st);
+}
+}  // namespace rc

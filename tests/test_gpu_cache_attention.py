@@ -155,28 +155,31 @@ def _without(cache, plan, kv, d, seq, pos, which, byte, block=1):
 @pytest.mark.parametrize("byte", [255, 254], ids=["nan", "inf"])
 @pytest.mark.parametrize("heads", [2, 8])
 def test_what_is_not_finite_reaches_the_rows_that_see_it_alone(dtype, which, byte, heads):
-    """A key or value of a token in the midst of a prompt: rows before it, and rows whose window has passed it, are
-    those of a cache without it; rows that see it are not finite where the formula is not."""
-    plan, kv, d, window = ref.Plan([(60, 75), (40, 40)], 16), 2, 128, 9
+    """A key or value of a token in the midst of a prompt: what the plain statement, which takes for a row what it
+    sees alone, gives as finite is finite and within the rounding, and what it does not is not."""
+    plan, kv, d = ref.Plan([(60, 75), (40, 40)], 16), 2, 128
     cache = ref.random_cache(plan, kv, d, 5)
     pos = 41
     bad = _without(cache, plan, kv, d, 0, pos, which, byte)
+    vals = [cache[2], cache[3]]
+    vals[which] = ref.values(bad).view(vals[which].shape)
     g = torch.Generator().manual_seed(9)
-    q = (torch.randn(plan.tokens, heads, d, generator=g).abs()).to(dtype).to(DEV)
-    caches = [(cache[0].to(DEV), cache[1].to(DEV)), (bad.to(DEV), cache[1].to(DEV)) if which == 0 else (cache[0].to(DEV), bad.to(DEV))]
-    clean, dirty = (rca.mxfp4_cache_attention(q, *c, *plan.tensors(DEV), window=window).float().cpu() for c in caches)
-    at = torch.tensor([-1 if s else p for s, p in plan.rows()])
-    sees = (at >= pos) & (at < pos + window)
-    assert torch.equal(clean[~sees], dirty[~sees])
-    assert torch.isfinite(dirty[~sees]).all()
-    if which == 1:
-        assert not torch.isfinite(dirty[sees][:, :, 32:64]).any()
-        assert torch.equal(clean[sees][:, :, :32], dirty[sees][:, :, :32])
-    elif byte == 255:
-        assert not torch.isfinite(dirty[sees]).any()
-    out, lse = rca.mxfp4_cache_attention(q, *caches[1], *plan.tensors(DEV), lse=True)
-    seen = at >= pos
-    assert torch.isfinite(out.cpu()[~seen]).all() and torch.isfinite(lse.cpu()[~seen]).all()
+    q = torch.randn(plan.tokens, heads, d, generator=g).abs().to(dtype)
+    caches = [cache[0].to(DEV), cache[1].to(DEV)]
+    caches[which] = bad.to(DEV)
+    for window in (0, 9):
+        got, lse = rca.mxfp4_cache_attention(q.to(DEV), *caches, *plan.tensors(DEV), window=window, lse=True)
+        out, ls, tol, lse_tol = ref.attention(plan, q, *vals, d ** -0.5, True, window)
+        fine = torch.isfinite(out)
+        sees = torch.tensor([not s and p >= pos and (window == 0 or p < pos + window) for s, p in plan.rows()])
+        assert fine[~sees].all() and not fine[sees].all()    # of the statement itself
+        got, lse = got.cpu().double(), lse.cpu().double()
+        assert not torch.isfinite(got[~fine]).any()
+        half, least = HALF[dtype]
+        bound = tol + (out.abs() + tol) * half + least
+        assert ((got - out).abs()[fine] <= bound[fine]).all()
+        fine = torch.isfinite(ls)
+        assert ((lse - ls).abs()[fine] <= lse_tol[fine]).all() and not torch.isfinite(lse[~fine]).any()
 
 
 @pytest.mark.parametrize("dtype", TYPES)
