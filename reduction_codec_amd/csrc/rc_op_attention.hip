@@ -1,23 +1,18 @@
-// Attention over a paged cache in MXFP4: the choice of kernels and the workspace.
+// Attention over a paged cache in MXFP4: the workspace and the type's kernels.
 #include "rc_op_attention.hpp"
 
 namespace rc {
 
-hipError_t launch_attention_bf16(int d, const CacheAttention& a, size_t most_rows, hipStream_t st);
-hipError_t launch_attention_fp16(int d, const CacheAttention& a, size_t most_rows, hipStream_t st);
-hipError_t launch_attention_fp32(int d, const CacheAttention& a, size_t most_rows, hipStream_t st);
+hipError_t launch_attention_bf16(int d, const CacheAttention& a, size_t rows, hipStream_t st);
+hipError_t launch_attention_fp16(int d, const CacheAttention& a, size_t rows, hipStream_t st);
+hipError_t launch_attention_fp32(int d, const CacheAttention& a, size_t rows, hipStream_t st);
 
-// By sizes alone, for the type that leaves the largest parts.
+// By sizes alone: the most that any type of queries takes.
 size_t cache_attention_work(size_t tokens, size_t heads, size_t kv_heads, size_t d)
 {
-    const int nb = (int)(d / 32), qt = tokens * (heads / kv_heads) <= 16 ? 1 : 2;
-    size_t most = 0;
-    for (int q = 1; q <= qt; ++q) {
-        const size_t groups = 256 * (size_t)row_groups(1, nb, q);
-        const size_t bytes = groups * (sizeof(Cut) + 2 * 16 * q * (d + 2) * sizeof(float));
-        most = bytes > most ? bytes : most;
-    }
-    return most;
+    const size_t rows = tokens > 0x7FFFFFFF ? tokens : tokens * (heads / kv_heads);
+    const size_t b = attention_work_t<kBF16>((int)d, rows), h = attention_work_t<kF16>((int)d, rows), f = attention_work_t<kF32>((int)d, rows);
+    return b > h ? (b > f ? b : f) : h > f ? h : f;
 }
 
 hipError_t launch_cache_attention(int dt, int d, const CacheAttention& a, size_t max_query, hipStream_t st)

@@ -55,50 +55,62 @@ struct RowMap {
     }
 };
 
-// A lane's part of sixteen tokens' codes.
+// A lane's part of sixteen tokens' codes, and words that hold its scales (a
+// byte's load would be widened as soon as it is there, and so waited for).
 template <int NB>
 struct Codes {
     uint32_t w[NB], s[RowMap<NB>::kPieces];
 };
 
-// Asks for tokens 16 k .. of a page's stream; lane (i, g) has token 16 k + i.
+// The scale byte of piece p, and the scale.
 template <int NB>
-__device__ __forceinline__ void load_codes(const uint8_t* stream, uint32_t k, uint32_t i, uint32_t g, Codes<NB>& c)
+__device__ __forceinline__ uint32_t scale_byte(const Codes<NB>& c, int p, uint32_t i, uint32_t g)
+{
+    return __builtin_amdgcn_ubfe(c.s[p], (i * NB + RowMap<NB>::block(p, g)) % 4 * 8, 8);
+}
+template <int NB>
+__device__ __forceinline__ float scale_of(const Codes<NB>& c, int p, uint32_t i, uint32_t g)
+{
+    return __uint_as_float(scale_byte<NB>(c, p, i, g) << 23);
+}
+
+// Asks for tokens 16 k .. of a head's stream in a page; lane (i, g) has token
+// 16 k + i.  Nothing is read, and all is zero, where the descriptor is empty.
+template <int NB>
+__device__ __forceinline__ void load_codes(Rsrc stream, uint32_t k, uint32_t i, uint32_t g, Codes<NB>& c)
 {
     typedef RowMap<NB> M;
-    const uint32_t b0 = 16 * NB * k, rem = NB % 4 == 0 ? 0 : b0 % 64;
-    const uint8_t* tile = stream + b0 / 64 * kMxTile;
+    // blocks 16 NB k ..: whole tiles, or a part of one, or (NB = 3, 6) of two
+    const uint32_t b0 = 16 * NB * k, tile = b0 / 64 * kMxTile, rem = b0 % 64;
+    constexpr bool kWhole = NB % 4 == 0, kPart = 64 % (16 * NB) == 0;
 #pragma unroll
     for (int p = 0; p < M::kPieces; ++p) {
-        const uint32_t b = rem + i * NB + M::block(p, g);
-        const uint8_t* at = tile + codes_at(b) + M::byte(p, g);
+        const uint32_t b = i * NB + M::block(p, g), r = kWhole || kPart ? b : rem + b;
+        const uint32_t codes = codes_at(r) + M::byte(p, g), soff = tile + (kPart ? rem * 16 : 0);
         if (M::words(p) == 4) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(at);
+            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(stream, codes, soff, 0);
 #pragma unroll
             for (int e = 0; e < 4; ++e) c.w[(M::first(p) + e) % NB] = v[e];
         } else if (M::words(p) == 2) {
-            const u32x2 v = *reinterpret_cast<const u32x2*>(at);
+            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(stream, codes, soff, 0);
             c.w[M::first(p)] = v.x;
             c.w[(M::first(p) + 1) % NB] = v.y;
         } else {
-            c.w[M::first(p)] = *reinterpret_cast<const uint32_t*>(at);
+            c.w[M::first(p)] = __builtin_amdgcn_raw_buffer_load_b32(stream, codes, soff, 0);
         }
-        c.s[p] = tile[scale_at(b)];
+        c.s[p] = __builtin_amdgcn_raw_buffer_load_b32(stream, scale_at(r) & ~3u, tile + (kPart ? rem : 0), 0);
     }
 }
 
-// ---- values in LDS: rows of D bfloat16 values, one a token, in 16-byte units
-// that are swizzled by the token so that the lanes of a store (eight tokens, one
-// unit) and of a transposing load (eight tokens, two units) fall on all banks.
-template <int NB>
-__device__ __forceinline__ uint32_t swizzle(uint32_t token)
-{
-    return NB % 4 == 0 ? (token & 7) * 2 : NB % 2 == 0 ? (token >> 1 & 3) * 2 : (token >> 2 & 1) * 2;
-}
+// ---- values in LDS: rows of D bfloat16 values, one a token, 32 bytes apart:
+// the lanes of a store (eight tokens, one 16-byte unit) and of a transposing
+// load (eight tokens, two units) then fall on all banks, D / 8 + 2 units being
+// 2, 10 or 14 modulo 16.
+template <int NB> constexpr uint32_t kValueRow = NB * 64 + 32;
 template <int NB>
 __device__ __forceinline__ uint32_t value_at(uint32_t token, uint32_t unit)
 {
-    return token * (NB * 64) + ((unit ^ swizzle<NB>(token)) << 4);
+    return token * kValueRow<NB> + unit * 16;
 }
 
 // Largest over the four lanes that share a row, in each of them.
@@ -109,14 +121,6 @@ __device__ __forceinline__ float max_of_row(float v)
     const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
-__device__ __forceinline__ float sum_of_row(float v)
-{
-    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
-}
-
 // Weights of 2 x 4 tokens as P bfloat16 terms that add up to them (to 2^-9,
 // 2^-17 and 2^-24 of themselves).
 template <int P>
@@ -146,38 +150,83 @@ __device__ __forceinline__ void wave_fence()
 
 // ---- work
 //
-// A sequence's items are its row tiles times the cache's heads, an item's units
-// its tokens 128 at a time; all units of all sequences stand in one row, and
-// workgroup w of W takes the w-th part of them, so that sequences of all lengths
-// load the card alike.  An item that is cut is joined by a second kernel: a
-// workgroup leaves at most two parts, of the item that it takes over (slot 2 w)
+// A sequence's rows are cut into tiles of R.  A tile has units of 128 tokens, as
+// many as its rows see; the first tile of a causal sequence sees the fewest and
+// the last the most, so tile j and the j-th from the end go together as a pair,
+// and all pairs of a sequence count alike (a pair may end in units that stand
+// for nothing).  All units of all pairs of all heads of all sequences stand in one
+// row, and workgroup w of W takes the w-th part of them, so that sequences of all
+// lengths load the card alike.  A tile that is cut is joined by a second kernel: a
+// workgroup leaves at most two parts, of the tile that it takes over (slot 2 w)
 // and of the one that it leaves (slot 2 w + 1).
 struct Sequence {
-    int row0, tokens, length, first;             // rows of q; tokens in the cache, and the first that any row sees
-    int units, tiles;                            // of an item; of rows
+    int row0, tokens, length;                    // first row of q; rows; tokens in the cache
 };
 
-template <int R>
-__device__ __forceinline__ Sequence sequence(const CacheAttention& a, int s)
+// Tiles of a sequence, and units of a pair of them (of the only one).
+struct Tiles {
+    int tiles, pairs;
+    int64_t units;                               // of a pair
+};
+
+// What the tile's rows see: the first token (a multiple of 32), and its units.
+struct Extent {
+    int first, units;
+};
+
+// The tokens that row r sees: lo <= j < hi.
+__device__ __forceinline__ void row_sees(const CacheAttention& a, const Sequence& q, uint32_t group, uint32_t r, int& lo, int& hi)
 {
-    Sequence q = {0, 0, 0, 0, 0, 0};
-    if (s >= a.c.seqs) return q;
-    const int lo = clamp_to(a.c.offsets[s], a.c.tokens), hi = clamp_to(a.c.offsets[s + 1], a.c.tokens);
-    if (hi <= lo) return q;
-    q.row0 = lo;
-    q.tokens = hi - lo;
-    q.length = a.c.pages == 0 ? 0 : seq_length(a.c, s);
-    const int64_t see = (int64_t)q.length - q.tokens - a.window + 1;
-    q.first = a.window != 0 && see > 0 ? (int)(see & ~(int64_t)31) : 0;
-    q.units = (q.length - q.first + kUnit - 1) / kUnit;
-    if (q.units < 1) q.units = 1;                // its rows are written all the same
-    q.tiles = (int)(((int64_t)q.tokens * (a.heads / a.c.kv_heads) + R - 1) / R);
-    return q;
+    const int64_t p = (int64_t)q.length - q.tokens + r / group;
+    hi = a.causal ? (p < q.length ? (int)(p + 1 < 0 ? 0 : p + 1) : q.length) : q.length;
+    lo = a.window != 0 && p - a.window + 1 > 0 ? (int)(p - a.window + 1) : 0;
 }
 
-// What a workgroup leaves of a cut item: where it starts, for the joining kernel.
+template <int R>
+__device__ __forceinline__ Extent extent(const CacheAttention& a, const Sequence& q, uint32_t group, int tile)
+{
+    const uint32_t rows = (uint32_t)q.tokens * group, r0 = (uint32_t)tile * R, r1 = rows - r0 < R ? rows : r0 + R;
+    int lo, hi, none;
+    row_sees(a, q, group, r0, lo, none);
+    row_sees(a, q, group, r1 - 1, none, hi);
+    lo &= ~31;
+    return {lo, hi > lo ? (hi - lo + kUnit - 1) / kUnit : 1};        // rows that see nothing are written all the same
+}
+
+template <int R>
+__device__ __forceinline__ Tiles tiles_of(const CacheAttention& a, const Sequence& q, uint32_t group)
+{
+    if (q.tokens == 0) return {0, 0, 0};
+    const int n = (int)(((uint32_t)q.tokens * group + R - 1) / R);
+    if (n == 1) return {1, 1, extent<R>(a, q, group, 0).units};
+    const int64_t whole = q.length > 0 ? ((int64_t)q.length + kUnit - 1) / kUnit : 1;
+    int64_t u = 2 * whole;
+    const int64_t before = (int64_t)q.length - q.tokens;
+    if (a.causal && before >= 0) {               // both ends' last rows, rounded up to units
+        const int64_t v = (2 * (before + 1) + ((int64_t)n + 1) * R / group) / kUnit + 2;
+        u = v < u ? v : u;
+    }
+    if (a.window != 0) {
+        const int64_t v = 2 * (((int64_t)a.window + R / group + 33) / kUnit + 2);
+        u = v < u ? v : u;
+    }
+    return {n, (n + 1) / 2, u};
+}
+
+// Sequence s if it is one of those with `least` < rows <= `most`.
+__device__ __forceinline__ Sequence sequence(const CacheAttention& a, int s, uint32_t group, uint32_t least, uint32_t most)
+{
+    Sequence q = {0, 0, 0};
+    if (s >= a.c.seqs) return q;
+    const int lo = clamp_to(a.c.offsets[s], a.c.tokens), hi = clamp_to(a.c.offsets[s + 1], a.c.tokens);
+    const uint32_t rows = hi > lo ? (uint32_t)(hi - lo) * group : 0;
+    if (rows <= least || rows > most) return q;
+    return {lo, hi - lo, a.c.pages == 0 ? 0 : seq_length(a.c, s)};
+}
+
+// What a workgroup leaves of a cut tile: where it starts, for the joining kernel.
 struct Cut {
-    int32_t row0, tokens, tile, head;            // as in the item; tokens = 0: nothing begins here
+    int32_t row0, tokens, tile, head;            // of the tile; tokens = 0: none begins here
     int32_t last, pad[3];                        // the last workgroup that has a part of it
 };
 
@@ -188,7 +237,7 @@ __device__ __forceinline__ float* part_of(float* work, unsigned groups, unsigned
     return work + (size_t)groups * (sizeof(Cut) / 4) + (size_t)slot * (R * (D + 2));
 }
 
-// Rows r of tile `tile` that there are, and where row r is written.
+// Rows of tile `tile` that there are, and where row r of q is written.
 __device__ __forceinline__ int rows_of(int tokens, int group, int tile, int R)
 {
     const int64_t left = (int64_t)tokens * group - (int64_t)tile * R;
@@ -204,7 +253,7 @@ template <int DT>
 __device__ __forceinline__ void write_values(const CacheAttention& a, size_t row, int d, int at, f32x4 v, float m, float l)
 {
     constexpr float kLn2 = 0.693147181f;
-    const float f = l == 0.0f ? 0.0f : 1.0f / l;
+    const float f = 1.0f / l;
     const f32x4 o = l == 0.0f ? f32x4{0, 0, 0, 0} : v * f;
     const size_t i = row * d + at;
     if constexpr (DT == kF32) *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + i) = o;
@@ -212,104 +261,152 @@ __device__ __forceinline__ void write_values(const CacheAttention& a, size_t row
     if (a.lse && at == 0) a.lse[row] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
 }
 
-// Workgroups of a compute unit (waves of a SIMD), by the registers that a lane
-// needs: queries, sums, two steps' codes, and some.
-constexpr int row_groups(int terms, int nb, int qt)
+// The weight that a part of maximum m has under the maximum `most`.
+__device__ __forceinline__ float under(float m, float most)
 {
-    const int regs = qt * (nb * 4 * terms + nb * 8) + 2 * (nb * 4 + 10) + 44;
-    return regs <= 128 ? 4 : regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
+    return most == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - most);
 }
 
-// Few rows an item: every wave takes 32 tokens of a unit, reads and decodes them
-// by itself and keeps 16 QT rows of q; the waves' sums meet at the item's end.
-// Keys go from memory to the registers that the matrix instructions read;
-// values pass through LDS, decoded, to be read transposed.
-template <int DT, int NB, int QT>
-__global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) void attention_rows_kernel(const CacheAttention a)
+// How the waves of a workgroup share a tile: its tokens, 32 of a unit each, for
+// 16 QT rows; or its rows, 16 QT each, for all tokens.
+enum class Share : int { kTokens, kRows };
+template <int QT, Share SH> constexpr int kTileRows = 16 * QT * (SH == Share::kRows ? kRowWaves : 1);
+
+// Workgroups of a compute unit (waves of a SIMD): by the registers that a lane
+// needs (queries, sums, scores, codes, and some), and by LDS.
+constexpr int row_groups(int terms, int nb, int qt)
 {
-    constexpr int D = 32 * NB, R = 16 * QT, P = Terms<DT>::v, ES = Elem<DT>::size, T = 64 * kRowWaves, ND = D / 16;
+    const int regs = qt * (nb * 4 * terms + nb * 8 + 8 + 4 * terms) + nb * 4 + 10 + 60;
+    const int by_regs = regs <= 128 ? 4 : regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
+    const int by_lds = 163840 / (kRowWaves * 32 * (nb * 64 + 32) + 4096);
+    return by_regs < by_lds ? by_regs : by_lds;
+}
+
+// Every wave reads and decodes its tokens by itself: keys go from memory to the
+// registers that the matrix instructions read; values pass through LDS, decoded,
+// to be read transposed.
+template <int DT, int NB, int QT, Share SH>
+__global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) void attention_kernel(
+    const CacheAttention a, float* work, uint32_t least, uint32_t most_rows)
+{
+    constexpr int D = 32 * NB, R = kTileRows<QT, SH>, P = Terms<DT>::v, ES = Elem<DT>::size, T = 64 * kRowWaves, ND = D / 16;
+    constexpr int kSeqs = 128;                   // sequences looked at at a time
+    constexpr int kStride = SH == Share::kTokens ? kUnit : 32;       // tokens from a wave's step to its next
     constexpr float kLog2e = 1.44269504f;
     typedef RowMap<NB> M;
-    __shared__ __attribute__((aligned(16))) uint8_t values[kRowWaves][32 * D * 2];
-    __shared__ int64_t before[T];                // units before each of 256 sequences
-    __shared__ Sequence seqs[T];
+    __shared__ __attribute__((aligned(16))) uint8_t values[kRowWaves][32 * kValueRow<NB>];
+    __shared__ int64_t before[kSeqs];            // units before each of them
+    __shared__ Sequence seqs[kSeqs];
     __shared__ int64_t sums[kRowWaves];
-    __shared__ float wave_max[kRowWaves][R], wave_sum[kRowWaves][R];
-    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, i = lane & 15, g = lane >> 4;
-    const int group = a.heads / a.c.kv_heads, kv = a.c.kv_heads;
-    const unsigned groups = gridDim.x;
+    __shared__ float wave_max[kRowWaves][16 * QT], wave_sum[kRowWaves][16 * QT];
+    const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
+    const uint32_t group = a.heads / a.c.kv_heads;
+    const int kv = a.c.kv_heads;
+    // the workgroups of an XCD, every eighth, take neighbouring parts: they share keys and values in its cache
+    const unsigned groups = gridDim.x, worker = blockIdx.x % 8 * (groups / 8) + blockIdx.x / 8;
 
-    // sequences s0 .. s0 + 255 to LDS, and their units' sum
-    auto look = [&](int s0) -> int64_t {
+    const auto units_of = [&](const Sequence& q) {
+        const Tiles t = tiles_of<R>(a, q, group);
+        return t.units * t.pairs * kv;
+    };
+    // sequences s0 .. to LDS, and their units' sum
+    const auto look = [&](int s0) -> int64_t {
         __syncthreads();
-        const Sequence q = sequence<R>(a, s0 + (int)tid);
-        seqs[tid] = q;
-        int64_t upto = (int64_t)q.units * q.tiles * kv;
-        const int64_t mine = upto;
+        int64_t upto = 0, mine = 0;
+        if (tid < kSeqs) {
+            const Sequence q = sequence(a, s0 + (int)tid, group, least, most_rows);
+            seqs[tid] = q;
+            upto = mine = units_of(q);
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int64_t v = __shfl_up(upto, d, 64);
-            if ((int)lane >= d) upto += v;
+            for (int d = 1; d < 64; d <<= 1) {
+                const int64_t v = __shfl_up(upto, d, 64);
+                if ((int)lane >= d) upto += v;
+            }
+            if (lane == 63) sums[wave] = upto;
         }
-        if (lane == 63) sums[wave] = upto;
         __syncthreads();
         int64_t total = 0;
 #pragma unroll
-        for (int w = 0; w < kRowWaves; ++w) {
+        for (int w = 0; w < kSeqs / 64; ++w) {
             if (w < (int)wave) upto += sums[w];
             total += sums[w];
         }
-        before[tid] = upto - mine;
+        if (tid < kSeqs) before[tid] = upto - mine;
         __syncthreads();
         return total;
     };
-    int64_t total = 0, base = 0, here = 0;       // units; before the sequences in LDS; of them
-    for (int s0 = 0; s0 < a.c.seqs; s0 += T) { here = look(s0); total += here; }
-    const int64_t workers = total < groups ? total : groups;
-    Cut* const cuts = reinterpret_cast<Cut*>(a.work);
-    if (tid == 0) cuts[blockIdx.x] = Cut{0, 0, 0, 0, 0, {0, 0, 0}};
-    if (blockIdx.x >= workers) return;
-    int64_t pos = total * blockIdx.x / workers;
-    const int64_t end = total * (blockIdx.x + 1) / workers;
-    int s0 = 0;
-    if (a.c.seqs > T) here = look(0);
-
-    uint8_t* const mine = values[wave];
-    while (pos < end) {
-        while (pos >= base + here) { base += here; s0 += T; here = look(s0); }
-        // the last sequence that begins at or before pos and has units
-        int lo = 0;
+    int64_t here = look(0), total = here, base = 0;                  // units of the sequences in LDS; all; before those
+    if (a.c.seqs > kSeqs) {
+        int64_t rest = 0;
+        for (int s = kSeqs + (int)tid; s < a.c.seqs; s += T) rest += units_of(sequence(a, s, group, least, most_rows));
 #pragma unroll
-        for (int step = T / 2; step > 0; step /= 2)
-            if (base + before[lo + step] <= pos) lo += step;
-        lo = __builtin_amdgcn_readfirstlane(lo);
-        const Sequence sq = seqs[lo];
-        const int row0 = __builtin_amdgcn_readfirstlane(sq.row0), tokens = __builtin_amdgcn_readfirstlane(sq.tokens);
-        const int length = __builtin_amdgcn_readfirstlane(sq.length), first = __builtin_amdgcn_readfirstlane(sq.first);
-        const int units = __builtin_amdgcn_readfirstlane(sq.units);
-        const int64_t rel = pos - base - before[lo], item = rel / units;
-        const int u0 = __builtin_amdgcn_readfirstlane((int)(rel - item * units));
-        const int head = __builtin_amdgcn_readfirstlane((int)(item % kv)), tile = __builtin_amdgcn_readfirstlane((int)(item / kv));
-        const int n = __builtin_amdgcn_readfirstlane((int)(end - pos < units - u0 ? end - pos : units - u0));
-        const int rows = rows_of(tokens, group, tile, R);
-        const uint32_t r0 = (uint32_t)tile * R;   // tokens * heads is below 2^31
+        for (int d = 1; d < 64; d <<= 1) rest += __shfl_xor(rest, d, 64);
+        if (lane == 0) sums[wave] = rest;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kRowWaves; ++w) total += sums[w];
+    }
+    const int64_t workers = total < groups ? total : groups;
+    Cut* const cuts = reinterpret_cast<Cut*>(work);
+    if (tid == 0) cuts[worker] = Cut{0, 0, 0, 0, 0, {0, 0, 0}};
+    if (worker >= workers) return;
+    int64_t pos = total * worker / workers;
+    const int64_t end = total * (worker + 1) / workers;
+    int s0 = 0;
+    uint8_t* const mine = values[wave];
 
-        // this lane's rows: their positions' bounds, their values cut into terms
-        u32x4 fq[QT][NB][P];
+    while (pos < end) {
+        while (pos >= base + here) { base += here; s0 += kSeqs; here = look(s0); }
+        int at = 0;                              // the last sequence that begins at or before pos
+#pragma unroll
+        for (int step = kSeqs / 2; step > 0; step /= 2)
+            if (base + before[at + step] <= pos) at += step;
+        at = __builtin_amdgcn_readfirstlane(at);
+        const Sequence sq = {__builtin_amdgcn_readfirstlane(seqs[at].row0), __builtin_amdgcn_readfirstlane(seqs[at].tokens),
+                             __builtin_amdgcn_readfirstlane(seqs[at].length)};
+        const Tiles tl = tiles_of<R>(a, sq, group);
+        const int64_t rel = pos - base - before[at], item = rel / tl.units, v = rel - item * tl.units;
+        const int head = __builtin_amdgcn_readfirstlane((int)(item / tl.pairs));
+        int tile = __builtin_amdgcn_readfirstlane((int)(item - (int64_t)head * tl.pairs));     // of a pair, the later one first
+        tile = tl.tiles - 1 - tile;
+        Extent ex = extent<R>(a, sq, group, tile);
+        int64_t u = v;
+        if (u >= ex.units) {
+            u -= ex.units;
+            tile = tl.tiles - 1 - tile;
+            if (tile * 2 + 1 == tl.tiles) ex.units = 0;              // the middle one is alone
+            else ex = extent<R>(a, sq, group, tile);
+        }
+        int64_t n64 = end - pos;
+        if (u >= ex.units) {                     // units that stand for nothing
+            pos += n64 < tl.units - v ? n64 : tl.units - v;
+            continue;
+        }
+        n64 = n64 < ex.units - u ? n64 : ex.units - u;
+        const int u0 = __builtin_amdgcn_readfirstlane((int)u), n = __builtin_amdgcn_readfirstlane((int)n64);
+        const int units = __builtin_amdgcn_readfirstlane(ex.units), first = __builtin_amdgcn_readfirstlane(ex.first);
+        tile = __builtin_amdgcn_readfirstlane(tile);
+        const int rows = rows_of(sq.tokens, group, tile, R);
+        // this wave's rows: from r0 on, `own` of them
+        const int skip = SH == Share::kRows ? (int)wave * 16 * QT : 0;
+        const uint32_t r0 = (uint32_t)tile * R + skip;
+        const int own = rows - skip < 16 * QT ? rows - skip : 16 * QT;
+
+        u32x4 fq[QT][NB][P];                     // cut into terms
         int see_lo[QT], see_hi[QT];
-        const auto bounds = [&](uint32_t r, int& lo_, int& hi_) {
-            const int64_t p = (int64_t)length - tokens + r / (uint32_t)group;
-            hi_ = a.causal ? (p < length ? (int)(p + 1 < 0 ? 0 : p + 1) : length) : length;
-            lo_ = a.window && p - a.window + 1 > 0 ? (int)(p - a.window + 1) : 0;
-        };
+        int all_lo = 0, all_hi = 0, any_lo = 0, any_hi = 0;          // what each of the rows sees, and what any does
+        if (own > 0) {
+            row_sees(a, sq, group, r0, any_lo, all_hi);
+            row_sees(a, sq, group, r0 + own - 1, all_lo, any_hi);
+        }
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-            const int r = 16 * t + i;
-            const bool in = r < rows;
-            const uint32_t rr = r0 + (in ? r : rows - 1);
-            bounds(rr, see_lo[t], see_hi[t]);
+            const int r = 16 * t + (int)i;
+            const bool in = r < own;
+            const uint32_t rr = r0 + (in ? r : 0);
+            row_sees(a, sq, group, rr, see_lo[t], see_hi[t]);
             const uint8_t* q = static_cast<const uint8_t*>(a.q) +
-                               ((size_t)(row0 + rr / (uint32_t)group) * a.q_stride + (size_t)(head * group + rr % (uint32_t)group) * D) * ES;
+                               ((size_t)(sq.row0 + rr / group) * a.q_stride + (size_t)(head * group + rr % group) * D) * ES;
             const uint32_t sign = a.scale < 0 ? 0x80008000u : 0;
 #pragma unroll
             for (int s = 0; s < NB; ++s) {
@@ -320,271 +417,357 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
                     for (int e = 0; e < 4; ++e) fq[t][s][p][e] ^= sign;
             }
         }
-        int all_lo, all_hi, any_lo, any_hi;       // what every row of the tile sees, and what any does
-        bounds(r0, any_lo, all_hi);
-        bounds(r0 + rows - 1, all_lo, any_hi);
         const float c = __builtin_fabsf(a.scale) * kLog2e;
 
         f32x4 acc[QT][ND];
-        float top[QT], sum[QT];                   // the running maximum in binary logarithms; this lane's part of the sum
+        f32x4 sum[QT];                           // the weights' sum, four times: a product with ones
+        float top[QT];                           // the running maximum in binary logarithms
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             top[t] = -__builtin_inff();
-            sum[t] = 0.0f;
+            sum[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int d = 0; d < ND; ++d) acc[t][d] = f32x4{0, 0, 0, 0};
         }
 
-        // the table's entries of this wave's next 32 steps, a lane a half step
-        const int seq = s0 + lo;
-        const int32_t* table = a.c.table + (size_t)seq * a.c.max_pages;
-        const int key0 = first + (u0 * kRowWaves + (int)wave) * 32;
-        int pages = -1;
-        auto look_up = [&](int step) {
-            const int64_t key = (int64_t)key0 + (int64_t)(step + (int)lane / 2) * kUnit + (lane & 1) * 16;
-            pages = key < length ? table[key >> a.c.shift] : -1;
-            if (pages >= a.c.pages) pages = -1;
-        };
-        struct Step { Codes<NB> k[2], v[2]; int page[2]; };
+        // this wave's steps of 32 tokens, from key0 on, kStride apart: those that its rows see
+        int key0 = first + u0 * kUnit, steps = n;
+        if constexpr (SH == Share::kTokens) {
+            key0 += (int)wave * 32;
+        } else {
+            const int key1 = key0 + n * kUnit;   // at most 2^30 + 127
+            key0 = any_lo > key0 ? any_lo & ~31 : key0;
+            const int last = any_hi < key1 ? any_hi : key1;
+            steps = last > key0 ? (last - key0 + 31) / 32 : 0;
+        }
+        if (sq.length == 0) steps = 0;           // it has no table and may have no page to read
+        // the table's entries of 32 steps, a lane a half step; a step's codes are asked for as soon as those of the
+        // step before are decoded
+        const int32_t* const table = a.c.table + (size_t)(s0 + at) * a.c.max_pages;
         const int mask16 = (1 << (a.c.shift - 4)) - 1;
-        auto load = [&](int step, Step& x) {
-            if ((step & 31) == 0) look_up(step);
+        int entries = -1, page[2] = {-1, -1};
+        const auto look_up = [&](int step) {     // the pages of step `step`, -1 where there is none
+            if ((step & 31) == 0) {
+                const int64_t key = (int64_t)key0 + (int64_t)(step + (int)lane / 2) * kStride + (lane & 1) * 16;
+                entries = key < sq.length ? table[key >> a.c.shift] : -1;
+                if (entries >= a.c.pages) entries = -1;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) page[h] = step < steps ? __builtin_amdgcn_readlane(entries, (step & 31) * 2 + h) : -1;
+        };
+        const auto load = [&](const uint8_t* cache, int step, Codes<NB> (&x)[2]) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                x.page[h] = __builtin_amdgcn_readlane(pages, (step & 31) * 2 + h);
-                const int key = key0 + step * kUnit + 16 * h;
-                const size_t at = stream_at(a.c, x.page[h] < 0 ? 0 : x.page[h], head);
-                const uint32_t k16 = (uint32_t)(key >> 4) & mask16;
-                load_codes<NB>(a.c.k + at, k16, i, g, x.k[h]);
-                load_codes<NB>(a.c.v + at, k16, i, g, x.v[h]);
+                const uint32_t k16 = (uint32_t)((key0 + step * kStride) / 16 + h) & mask16;
+                const Rsrc r = span_rsrc(cache, stream_at(a.c, page[h] < 0 ? 0 : page[h], head), page[h] < 0 ? 0 : a.c.head_bytes);
+                load_codes<NB>(r, k16, i, g, x[h]);
             }
         };
-        auto compute = [&](int step, Step& x) {
-            const int key = key0 + step * kUnit;
-            const bool full = x.page[0] >= 0 && x.page[1] >= 0 && key >= all_lo && key + 32 <= all_hi;
-            bool odd = false;                     // values that may not be finite where some row does not see them
-            if (!full) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int mine_key = key + 16 * h + (int)i;
-                    const bool in = x.page[h] >= 0 && mine_key >= any_lo && mine_key < any_hi;
-#pragma unroll
-                    for (int s = 0; s < NB; ++s) x.v[h].w[s] = in ? x.v[h].w[s] : 0;
-#pragma unroll
-                    for (int p = 0; p < M::kPieces; ++p) {
-                        x.v[h].s[p] = in ? x.v[h].s[p] : 127;
-                        odd |= x.v[h].s[p] >= 253;
-                    }
-                }
-                odd = __builtin_amdgcn_ballot_w64(odd) != 0;
-            }
+        Codes<NB> xk[2], xv[2];
+        if (steps > 0) {
+            look_up(0);
+            load(a.c.k, 0, xk);
+            load(a.c.v, 0, xv);
+        }
+        for (int step = 0; step < steps; ++step) {
+            const int key = key0 + step * kStride;
+            const bool there[2] = {page[0] >= 0, page[1] >= 0};
+            const bool full = there[0] && there[1] && key >= all_lo && key + 32 <= all_hi;
             f32x4 score[QT][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int t = 0; t < 2 * QT; ++t) score[t / 2][t % 2] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int t = 0; t < QT; ++t) score[t][h] = f32x4{0, 0, 0, 0};
+            for (int s = 0; s < NB; ++s)
 #pragma unroll
-                for (int s = 0; s < NB; ++s) {
-                    const u32x4 fk = decode8(x.k[h].w[s], __uint_as_float(x.k[h].s[M::piece(s)] << 23));
+                for (int h = 0; h < 2; ++h) {
+                    const u32x4 fk = decode8(xk[h].w[s], scale_of<NB>(xk[h], M::piece(s), i, g));
 #pragma unroll
                     for (int t = 0; t < QT; ++t)
 #pragma unroll
                         for (int p = 0; p < P; ++p) score[t][h] = mfma<false>(fk, fq[t][s][p], score[t][h]);
                 }
+            look_up(step + 1);
+            load(a.c.k, step + 1, xk);
+            bool odd = false;                     // values that may not be finite where some row does not see them
+            if (!full) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int mine_key = key + 16 * h + (int)i;
+                    const bool in = there[h] && mine_key >= any_lo && mine_key < any_hi;
+#pragma unroll
+                    for (int s = 0; s < NB; ++s) xv[h].w[s] = in ? xv[h].w[s] : 0;
+#pragma unroll
+                    for (int p = 0; p < M::kPieces; ++p) {
+                        xv[h].s[p] = in ? xv[h].s[p] : 0x7F7F7F7F;
+                        odd |= scale_byte<NB>(xv[h], p, i, g) >= 253;
+                    }
+                }
+                odd = __builtin_amdgcn_ballot_w64(odd) != 0;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int s = 0; s < NB; ++s)
                     *reinterpret_cast<u32x4*>(mine + value_at<NB>(16 * h + i, M::unit(s, g))) =
-                        decode8(x.v[h].w[s], __uint_as_float(x.v[h].s[M::piece(s)] << 23));
-            }
+                        decode8(xv[h].w[s], scale_of<NB>(xv[h], M::piece(s), i, g));
             wave_fence();
-            u32x4 fp[QT][P];
-            uint32_t seen[QT];
+            load(a.c.v, step + 1, xv);
+            // the first values are read while the weights are formed
+            const uint8_t* const column = mine + value_at<NB>(4 * g + i / 4, i % 4 / 2) + i % 2 * 8;
+            constexpr int kAhead = ND < 8 ? ND : 8;
+            u32x4 fv[kAhead];
+#pragma unroll
+            for (int d = 0; d < kAhead; ++d) fv[d] = load_columns(column + 32 * d, 16 * kValueRow<NB>);
+            __builtin_amdgcn_sched_barrier(0);
+            // weights under the maximum so far, which may lag behind by 2^8; where that is not enough, or some row does
+            // not see all, the maximum is moved, and what is summed under it
+            float p[QT][8];
+            bool late = false;                   // (of any lane: one test of the wave)
 #pragma unroll
             for (int t = 0; t < QT; ++t) {
-                float p[8];
-                float cc = c;
-                seen[t] = 0xFF;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) p[e] = score[t][e / 4][e % 4];
-                if (!full) {
-                    seen[t] = 0;
+                for (int e = 0; e < 8; ++e) p[t][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(score[t][e / 4][e % 4], c, -top[t]));
+                late |= fmaxf(fmaxf(fmaxf(fmaxf(p[t][0], p[t][1]), p[t][2]), fmaxf(fmaxf(p[t][3], p[t][4]), p[t][5])), fmaxf(p[t][6], p[t][7])) > 256.0f;
+            }
+            if (__builtin_expect(__builtin_amdgcn_ballot_w64(late | !full) != 0, 0)) {
+#pragma unroll
+                for (int t = 0; t < QT; ++t) {
+                    float most = top[t];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const int k = key + 16 * (e / 4) + 4 * (int)g + e % 4;
-                        const bool in = x.page[e / 4] >= 0 && k >= see_lo[t] && k < see_hi[t];
-                        seen[t] |= in ? 1u << e : 0;
-                        p[e] = in ? p[e] * c : -__builtin_inff();
+                        const bool in = there[e / 4] && k >= see_lo[t] && k < see_hi[t];
+                        p[t][e] = in ? score[t][e / 4][e % 4] * c : -__builtin_inff();
+                        most = fmaxf(most, p[t][e]);
                     }
-                    cc = 1.0f;
-                }
-                float most = fmaxf(fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3])), fmaxf(fmaxf(p[4], p[5]), fmaxf(p[6], p[7]))) * cc;
-                // the maximum may lag by 2^8: it is moved, and what is summed with it, only when it has to be
-                if (__builtin_amdgcn_ballot_w64(most > top[t] + 8.0f) != 0) {
-                    most = fmaxf(max_of_row(most), top[t]);
-                    const float old = most == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f(top[t] - most);
+                    most = max_of_row(most);
+                    const float base = most == -__builtin_inff() ? 0.0f : most, f = most == base ? __builtin_amdgcn_exp2f(top[t] - most) : 1.0f;
                     top[t] = most;
-                    sum[t] *= old;
 #pragma unroll
-                    for (int d = 0; d < ND; ++d) acc[t][d] *= old;
+                    for (int d = 0; d < ND; ++d) acc[t][d] *= f;
+                    sum[t] *= f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) p[t][e] = __builtin_amdgcn_exp2f(p[t][e] - base);
                 }
-                const float m = top[t] == -__builtin_inff() ? 0.0f : top[t];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[e], cc, -m));
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum[t] += p[e];
-                cut_weights<P>(p, fp[t]);
             }
-            auto products = [&](int d, u32x4 fv) {
+            u32x4 fp[QT][P];
 #pragma unroll
-                for (int t = 0; t < QT; ++t)
+            for (int t = 0; t < QT; ++t) {
+                cut_weights<P>(p[t], fp[t]);
 #pragma unroll
-                    for (int p = 0; p < P; ++p) acc[t][d] = mfma<false>(fv, fp[t][p], acc[t][d]);
-            };
+                for (int x = 0; x < P; ++x) sum[t] = mfma<false>(u32x4{0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80}, fp[t][x], sum[t]);
+            }
             if (!odd) {
 #pragma unroll
-                for (int d = 0; d < ND; ++d)
-                    products(d, load_columns(mine + value_at<NB>(4 * g + i / 4, 2 * d + i % 4 / 2) + i % 2 * 8, 16 * D * 2));
+                for (int d = 0; d < ND; ++d) {
+#pragma unroll
+                    for (int t = 0; t < QT; ++t)
+#pragma unroll
+                        for (int p = 0; p < P; ++p) acc[t][d] = mfma<false>(fv[d % kAhead], fp[t][p], acc[t][d]);
+                    if (d + kAhead < ND) fv[d % kAhead] = load_columns(column + 32 * (d + kAhead), 16 * kValueRow<NB>);
+                }
             } else {                              // token by token, for the rows that see it alone
+#pragma unroll 1
                 for (int k = 0; k < 32; ++k) {
-                    const bool held = (int)g == k % 16 / 4;
-                    const int word = k / 16 * 2 + k % 4 / 2;
-                    const uint32_t keep = k % 2 ? 0xFFFF0000u : 0x0000FFFFu;
+                    const uint32_t keep = (int)g != k % 16 / 4 ? 0 : k % 2 ? 0xFFFF0000u : 0x0000FFFFu;
 #pragma unroll
                     for (int d = 0; d < ND; ++d) {
-                        u32x4 fv = load_columns(mine + value_at<NB>(4 * g + i / 4, 2 * d + i % 4 / 2) + i % 2 * 8, 16 * D * 2);
+                        u32x4 f1 = load_columns(column + 32 * d, 16 * kValueRow<NB>);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) fv[e] = held && e == word ? fv[e] & keep : 0;
+                        for (int e = 0; e < 4; ++e) f1[e] &= e == k / 16 * 2 + k % 4 / 2 ? keep : 0;
 #pragma unroll
                         for (int t = 0; t < QT; ++t) {
                             f32x4 one = {0, 0, 0, 0};
 #pragma unroll
-                            for (int p = 0; p < P; ++p) one = mfma<false>(fv, fp[t][p], one);
-                            // the row's lane that has the token's score says whether it is seen
-                            const uint32_t bits = (uint32_t)__shfl((int)seen[t], (int)(k % 16 / 4 * 16 + i), 64);
-                            const bool in = bits >> (k / 16 * 4 + k % 4) & 1;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) acc[t][d][e] = in ? acc[t][d][e] + one[e] : acc[t][d][e];
+                            for (int p = 0; p < P; ++p) one = mfma<false>(f1, fp[t][p], one);
+                            const bool in = key + k >= see_lo[t] && key + k < see_hi[t];
+                            acc[t][d] = in ? acc[t][d] + one : acc[t][d];
                         }
                     }
                 }
             }
             wave_fence();
-        };
-        Step x, y;
-        const int steps = length > 0 ? n : 0;    // an empty sequence has no table and may have no page to read
-        if (steps > 0) load(0, x);
-        for (int step = 0; step < steps; step += 2) {
-            if (step + 1 < steps) load(step + 1, y);
-            compute(step, x);
-            if (step + 1 >= steps) break;
-            if (step + 2 < steps) load(step + 2, x);
-            compute(step + 1, y);
         }
 
-        // the waves' sums meet
-#pragma unroll
-        for (int t = 0; t < QT; ++t) {
-            sum[t] = sum_of_row(sum[t]);
-            if (g == 0) { wave_max[wave][16 * t + i] = top[t]; wave_sum[wave][16 * t + i] = sum[t]; }
-        }
-        __syncthreads();
         const bool whole = u0 == 0 && n == units;
-        float* const part = part_of<D, R>(a.work, groups, 2 * blockIdx.x + (u0 == 0 ? 1 : 0));
+        float* const part = part_of<D, R>(work, groups, 2 * worker + (u0 == 0 ? 1 : 0));
+        // row r of 16, values 4 u .. of it: their sum, the maximum and the weights' sum
+        const auto put = [&](int r, int u, f32x4 x, float m, float l) {
+            if (whole) {
+                write_values<DT>(a, out_row(sq.row0, group, a.heads, head, r0 + r), D, u * 4, x, m, l);
+            } else {
+                *reinterpret_cast<f32x4*>(part + (skip + r) * D + u * 4) = x;
+                if (u == 0) { part[R * D + skip + r] = m; part[R * D + R + skip + r] = l; }
+            }
+        };
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-            float most = wave_max[0][16 * t + i];
-#pragma unroll
-            for (int w = 1; w < kRowWaves; ++w) most = fmaxf(most, wave_max[w][16 * t + i]);
-            const float f = most == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(top[t] - most);
-            float* const o = reinterpret_cast<float*>(mine);        // 16 rows of D sums
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-                *reinterpret_cast<f32x4*>(o + i * D + (((4 * d + g) ^ (i & 7)) << 2)) = acc[t][d] * f;
+            if (g == 0) { wave_max[wave][16 * t + i] = top[t]; wave_sum[wave][16 * t + i] = sum[t][0]; }
+        }
+        float* const o = reinterpret_cast<float*>(mine);             // 16 rows of D sums, 16 bytes apart
+        if constexpr (SH == Share::kTokens) {    // the waves' sums meet
             __syncthreads();
-            for (int e = tid; e < 16 * (D / 4); e += T) {
-                const int r = e / (D / 4), u = e % (D / 4);
-                if (16 * t + r >= rows) continue;
-                f32x4 v = {0, 0, 0, 0};
-                float m = -__builtin_inff(), l = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kRowWaves; ++w) {
-                    v += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(values[w]) + r * D + ((u ^ (r & 7)) << 2));
-                    m = fmaxf(m, wave_max[w][16 * t + r]);
-                }
+            for (int t = 0; t < QT; ++t) {
+                float most = wave_max[0][16 * t + i];
 #pragma unroll
-                for (int w = 0; w < kRowWaves; ++w)
-                    l += wave_sum[w][16 * t + r] * (m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(wave_max[w][16 * t + r] - m));
-                if (whole) {
-                    const size_t at = out_row(row0, group, a.heads, head, r0 + 16 * t + r);
-                    write_values<DT>(a, at, D, u * 4, v, m, l);
-                } else {
-                    *reinterpret_cast<f32x4*>(part + (16 * t + r) * D + u * 4) = v;
-                    if (u == 0) { part[R * D + 16 * t + r] = m; part[R * D + R + 16 * t + r] = l; }
+                for (int w = 1; w < kRowWaves; ++w) most = fmaxf(most, wave_max[w][16 * t + i]);
+                const float f = under(top[t], most);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4*>(o + i * (D + 4) + 16 * d + 4 * g) = acc[t][d] * f;
+                __syncthreads();
+                for (int e = tid; e < 16 * (D / 4); e += T) {
+                    const int r = e / (D / 4), u = e % (D / 4);
+                    if (16 * t + r >= own) continue;
+                    f32x4 x = {0, 0, 0, 0};
+                    float m = -__builtin_inff(), l = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kRowWaves; ++w) {
+                        x += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(values[w]) + r * (D + 4) + u * 4);
+                        m = fmaxf(m, wave_max[w][16 * t + r]);
+                    }
+#pragma unroll
+                    for (int w = 0; w < kRowWaves; ++w) l += wave_sum[w][16 * t + r] * under(wave_max[w][16 * t + r], m);
+                    put(16 * t + r, u, x, m, l);
                 }
+                __syncthreads();
             }
-            __syncthreads();
+        } else {
+#pragma unroll
+            for (int t = 0; t < QT; ++t) {
+#pragma unroll
+                for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4*>(o + i * (D + 4) + 16 * d + 4 * g) = acc[t][d];
+                wave_fence();
+                for (int e = lane; e < 16 * (D / 4); e += 64) {
+                    const int r = e / (D / 4), u = e % (D / 4);
+                    if (16 * t + r < own)
+                        put(16 * t + r, u, *reinterpret_cast<const f32x4*>(o + r * (D + 4) + u * 4), wave_max[wave][16 * t + r],
+                            wave_sum[wave][16 * t + r]);
+                }
+                wave_fence();
+            }
         }
         if (u0 == 0 && !whole && tid == 0) {
-            const int64_t last = pos + units - 1;                   // the item's last unit
-            cuts[blockIdx.x] = Cut{row0, tokens, tile, head, (int)(((last + 1) * workers - 1) / total), {0, 0, 0}};
+            const int64_t last = pos + units - 1;                    // the tile's last unit
+            cuts[worker] = Cut{sq.row0, sq.tokens, tile, head, (int)(((last + 1) * workers - 1) / total), {0, 0, 0}};
         }
         pos += n;
     }
 }
 
-// Joins the parts of an item that begins in workgroup blockIdx.x and is cut: a wave a row.
-template <int DT, int NB, int QT>
-__global__ __launch_bounds__(64 * kRowWaves) void attention_join_kernel(const CacheAttention a, unsigned groups)
+// Joins the parts of a tile that begins in workgroup blockIdx.x and is cut,
+// blockIdx.y's rows of it.  The lanes of D / 4 values take the parts in turn, so
+// that few rows of many parts wait for memory once.
+constexpr int kJoinRows = 4;                     // workgroups in y
+template <int DT, int NB, int QT, Share SH>
+__global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttention a, const float* work, unsigned groups)
 {
-    constexpr int D = 32 * NB, R = 16 * QT;
-    const Cut cut = reinterpret_cast<const Cut*>(a.work)[blockIdx.x];
+    constexpr int D = 32 * NB, R = kTileRows<QT, SH>, L = D / 4, S = 256 / L;
+    __shared__ f32x4 sums[S][L];
+    __shared__ float maxima[4], weights[S];
+    const Cut cut = reinterpret_cast<const Cut*>(work)[blockIdx.x];
     if (cut.tokens == 0) return;
-    const int lane = threadIdx.x & 63, group = a.heads / a.c.kv_heads, rows = rows_of(cut.tokens, group, cut.tile, R);
-    const int count = cut.last - (int)blockIdx.x + 1;
-    const auto part = [&](int x) { return part_of<D, R>(a.work, groups, 2 * (blockIdx.x + x) + (x == 0 ? 1 : 0)); };
-    for (int r = threadIdx.x >> 6; r < rows; r += kRowWaves) {
+    const int tid = threadIdx.x, stripe = tid / L, at = tid % L, group = a.heads / a.c.kv_heads;
+    const int rows = rows_of(cut.tokens, group, cut.tile, R), count = cut.last - (int)blockIdx.x + 1;
+    const auto part = [&](int x) { return part_of<D, R>(const_cast<float*>(work), groups, 2 * (blockIdx.x + x) + (x == 0 ? 1 : 0)); };
+    for (int r = blockIdx.y; r < rows; r += kJoinRows) {
         float m = -__builtin_inff();
-        for (int x = lane; x < count; x += 64) m = fmaxf(m, part(x)[R * D + r]);
+        for (int x = tid; x < count; x += 256) m = fmaxf(m, part(x)[R * D + r]);
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+        if (tid % 64 == 0) maxima[tid / 64] = m;
+        __syncthreads();
+        m = fmaxf(fmaxf(maxima[0], maxima[1]), fmaxf(maxima[2], maxima[3]));
         float l = 0.0f;
         f32x4 v = {0, 0, 0, 0};
-        for (int x = 0; x < count; ++x) {
-            const float* p = part(x);
-            const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(p[R * D + r] - m);
-            l += p[R * D + R + r] * f;
-            if (lane < D / 4) v += *reinterpret_cast<const f32x4*>(p + r * D + lane * 4) * f;
+        if (stripe < S) {
+#pragma unroll 4
+            for (int x = stripe; x < count; x += S) {
+                const float* p = part(x);
+                const float f = under(p[R * D + r], m);
+                l += p[R * D + R + r] * f;
+                v += *reinterpret_cast<const f32x4*>(p + r * D + at * 4) * f;
+            }
+            sums[stripe][at] = v;
+            if (at == 0) weights[stripe] = l;
         }
-        if (lane < D / 4) write_values<DT>(a, out_row(cut.row0, group, a.heads, cut.head, (uint32_t)cut.tile * R + r), D, lane * 4, v, m, l);
+        __syncthreads();
+        if (stripe == 0) {
+#pragma unroll
+            for (int x = 1; x < S; ++x) { v += sums[x][at]; l += weights[x]; }
+            write_values<DT>(a, out_row(cut.row0, group, a.heads, cut.head, (uint32_t)cut.tile * R + r), D, at * 4, v, m, l);
+        }
+        __syncthreads();
     }
 }
 
-template <int DT, int NB, int QT>
-hipError_t attention_rows(const CacheAttention& a, hipStream_t st)
+// Workgroups of a launch, and its workspace.
+template <int DT, int NB, int QT> constexpr unsigned kGroups = 256 * row_groups(Terms<DT>::v, NB, QT);
+template <int DT, int NB, int QT, Share SH>
+constexpr size_t attention_bytes()
 {
-    constexpr unsigned W = 256 * row_groups(Terms<DT>::v, NB, QT);
-    attention_rows_kernel<DT, NB, QT><<<W, 64 * kRowWaves, 0, st>>>(a);
+    return kGroups<DT, NB, QT> * (sizeof(Cut) + 2 * kTileRows<QT, SH> * (32 * NB + 2) * sizeof(float));
+}
+
+template <int DT, int NB, int QT, Share SH>
+hipError_t attention_launch(const CacheAttention& a, float* work, size_t least, size_t most, hipStream_t st)
+{
+    constexpr unsigned W = kGroups<DT, NB, QT>;
+    attention_kernel<DT, NB, QT, SH><<<W, 64 * kRowWaves, 0, st>>>(a, work, (uint32_t)least, (uint32_t)(most < 0x7FFFFFFF ? most : 0x7FFFFFFF));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attention_join_kernel<DT, NB, QT><<<W, 64 * kRowWaves, 0, st>>>(a, W);
+    attention_join_kernel<DT, NB, QT, SH><<<dim3(W, kJoinRows), 256, 0, st>>>(a, work, W);
     return hipGetLastError();
 }
 
+// Rows of a sequence up to which the waves share its tokens.
+constexpr size_t kFewRows = 32;
+
+// `rows`: no sequence has more rows of q a head.
 template <int DT, int NB>
-hipError_t attention_d(const CacheAttention& a, size_t most_rows, hipStream_t st)
+hipError_t attention_d(const CacheAttention& a, size_t rows, hipStream_t st)
 {
-    return most_rows <= 16 ? attention_rows<DT, NB, 1>(a, st) : attention_rows<DT, NB, 2>(a, st);
+    if (rows <= 16) return attention_launch<DT, NB, 1, Share::kTokens>(a, a.work, 0, ~(size_t)0, st);
+    if (rows <= kFewRows) return attention_launch<DT, NB, 2, Share::kTokens>(a, a.work, 0, ~(size_t)0, st);
+    if (a.c.seqs == 1) return attention_launch<DT, NB, 2, Share::kRows>(a, a.work, 0, ~(size_t)0, st);
+    const hipError_t e = attention_launch<DT, NB, 2, Share::kRows>(a, a.work, kFewRows, ~(size_t)0, st);
+    if (e != hipSuccess) return e;
+    return attention_launch<DT, NB, 2, Share::kTokens>(a, a.work + attention_bytes<DT, NB, 2, Share::kRows>() / 4, 0, kFewRows, st);
+}
+
+template <int DT, int NB>
+size_t attention_work_d(size_t rows)
+{
+    const size_t few = attention_bytes<DT, NB, 1, Share::kTokens>(), some = attention_bytes<DT, NB, 2, Share::kTokens>();
+    if (rows <= 16) return few;
+    // a hint may ask for the kernel of 16 rows all the same
+    if (rows <= kFewRows) return some > few ? some : few;
+    const size_t many = attention_bytes<DT, NB, 2, Share::kRows>() + some;
+    return many > few ? many : few;
 }
 
 template <int DT>
-hipError_t attention_t(int d, const CacheAttention& a, size_t most_rows, hipStream_t st)
+hipError_t attention_t(int d, const CacheAttention& a, size_t rows, hipStream_t st)
 {
     switch (d) {
-    case 64: return attention_d<DT, 2>(a, most_rows, st);
-    case 96: return attention_d<DT, 3>(a, most_rows, st);
-    case 128: return attention_d<DT, 4>(a, most_rows, st);
-    case 192: return attention_d<DT, 6>(a, most_rows, st);
-    default: return attention_d<DT, 8>(a, most_rows, st);
+    case 64: return attention_d<DT, 2>(a, rows, st);
+    case 96: return attention_d<DT, 3>(a, rows, st);
+    case 128: return attention_d<DT, 4>(a, rows, st);
+    case 192: return attention_d<DT, 6>(a, rows, st);
+    default: return attention_d<DT, 8>(a, rows, st);
+    }
+}
+
+template <int DT>
+size_t attention_work_t(int d, size_t rows)
+{
+    switch (d) {
+    case 64: return attention_work_d<DT, 2>(rows);
+    case 96: return attention_work_d<DT, 3>(rows);
+    case 128: return attention_work_d<DT, 4>(rows);
+    case 192: return attention_work_d<DT, 6>(rows);
+    case 256: return attention_work_d<DT, 8>(rows);
+    default: return 0;
     }
 }
 

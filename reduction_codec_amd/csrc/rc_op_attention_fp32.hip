@@ -2,8 +2,10 @@
 #include "rc_op_attention.hpp"
 
 namespace rc {
-hipError_t launch_attention_fp32(int d, const CacheAttention& a, size_t most_rows, hipStream_t st)
+
+hipError_t launch_attention_fp32(int d, const CacheAttention& a, size_t rows, hipStream_t st)
 {
-    return attention_t<kF32>(d, a, most_rows, st);
+    return attention_t<kF32>(d, a, rows, st);
 }
+
 }  // namespace rc
