@@ -74,31 +74,42 @@ __device__ __forceinline__ float scale_of(const Codes<NB>& c, int p, uint32_t i,
     return __uint_as_float(scale_byte<NB>(c, p, i, g) << 23);
 }
 
-// Asks for tokens 16 k .. of a head's stream in a page; lane (i, g) has token
-// 16 k + i.  Nothing is read, and all is zero, where the descriptor is empty.
+// Where sixteen tokens' codes lie in the cache: the byte of the tile that they
+// begin in, and, below its 16, how many sixteens of blocks into it (of 96 and 192
+// values sixteen tokens are no whole tiles) and whether there is no such page.
+constexpr uint32_t kNoPage = 4;
 template <int NB>
-__device__ __forceinline__ void load_codes(Rsrc stream, uint32_t k, uint32_t i, uint32_t g, Codes<NB>& c)
+__device__ __forceinline__ uint64_t group_at(const Cache& c, int page, int head, uint32_t k16)
+{
+    if (page < 0 || page >= c.pages) return kNoPage;
+    const uint32_t b0 = 16 * NB * k16;
+    return stream_at(c, page, head) + b0 / 64 * kMxTile + b0 % 64 / 16;
+}
+
+// Asks for them; lane (i, g) has token i of the sixteen.
+template <int NB>
+__device__ __forceinline__ void load_codes(const uint8_t* cache, uint64_t where, uint32_t i, uint32_t g, Codes<NB>& c)
 {
     typedef RowMap<NB> M;
-    // blocks 16 NB k ..: whole tiles, or a part of one, or (NB = 3, 6) of two
-    const uint32_t b0 = 16 * NB * k, tile = b0 / 64 * kMxTile, rem = b0 % 64;
-    constexpr bool kWhole = NB % 4 == 0, kPart = 64 % (16 * NB) == 0;
+    constexpr bool kWhole = NB % 4 == 0, kPart = 64 % (16 * NB) == 0;        // whole tiles; a part of one, or (NB = 3, 6) of two
+    const uint32_t rem = kWhole ? 0 : ((uint32_t)where & 3) * 16;
+    const uint8_t* const tile = cache + (where & ~(uint64_t)15);
 #pragma unroll
     for (int p = 0; p < M::kPieces; ++p) {
         const uint32_t b = i * NB + M::block(p, g), r = kWhole || kPart ? b : rem + b;
-        const uint32_t codes = codes_at(r) + M::byte(p, g), soff = tile + (kPart ? rem * 16 : 0);
+        const uint8_t* const at = tile + (kPart ? rem * 16 : 0) + (codes_at(r) + M::byte(p, g));
         if (M::words(p) == 4) {
-            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(stream, codes, soff, 0);
+            const u32x4 v = *reinterpret_cast<const u32x4*>(at);
 #pragma unroll
             for (int e = 0; e < 4; ++e) c.w[(M::first(p) + e) % NB] = v[e];
         } else if (M::words(p) == 2) {
-            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(stream, codes, soff, 0);
+            const u32x2 v = *reinterpret_cast<const u32x2*>(at);
             c.w[M::first(p)] = v.x;
             c.w[(M::first(p) + 1) % NB] = v.y;
         } else {
-            c.w[M::first(p)] = __builtin_amdgcn_raw_buffer_load_b32(stream, codes, soff, 0);
+            c.w[M::first(p)] = *reinterpret_cast<const uint32_t*>(at);
         }
-        c.s[p] = __builtin_amdgcn_raw_buffer_load_b32(stream, scale_at(r) & ~3u, tile + (kPart ? rem : 0), 0);
+        c.s[p] = *reinterpret_cast<const uint32_t*>(tile + (kPart ? rem : 0) + (scale_at(r) & ~3u));
     }
 }
 
@@ -276,7 +287,7 @@ template <int QT, Share SH> constexpr int kTileRows = 16 * QT * (SH == Share::kR
 // needs (queries, sums, scores, codes, and some), and by LDS.
 constexpr int row_groups(int terms, int nb, int qt)
 {
-    const int regs = qt * (nb * 4 * terms + nb * 8 + 8 + 4 * terms) + nb * 4 + 10 + 60;
+    const int regs = qt * (nb * 4 * terms + nb * 8 + 8 + 4 * terms) + nb * 4 + 10 + 60 + (qt == 1 ? nb * 4 + 10 : 0);
     const int by_regs = regs <= 128 ? 4 : regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
     const int by_lds = 163840 / (kRowWaves * 32 * (nb * 64 + 32) + 4096);
     return by_regs < by_lds ? by_regs : by_lds;
@@ -292,6 +303,7 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
     constexpr int D = 32 * NB, R = kTileRows<QT, SH>, P = Terms<DT>::v, ES = Elem<DT>::size, T = 64 * kRowWaves, ND = D / 16;
     constexpr int kSeqs = 128;                   // sequences looked at at a time
     constexpr int kStride = SH == Share::kTokens ? kUnit : 32;       // tokens from a wave's step to its next
+    constexpr int kDepth = SH == Share::kTokens && QT == 1 ? 2 : 1;  // steps asked for ahead
     constexpr float kLog2e = 1.44269504f;
     typedef RowMap<NB> M;
     __shared__ __attribute__((aligned(16))) uint8_t values[kRowWaves][32 * kValueRow<NB>];
@@ -441,37 +453,38 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
             steps = last > key0 ? (last - key0 + 31) / 32 : 0;
         }
         if (sq.length == 0) steps = 0;           // it has no table and may have no page to read
-        // the table's entries of 32 steps, a lane a half step; a step's codes are asked for as soon as those of the
-        // step before are decoded
+        // where the codes of 32 steps lie, a lane a half step; a step's codes are asked for as soon as those that lie in
+        // the same registers, kDepth steps before, are decoded (after the last step, its own again)
         const int32_t* const table = a.c.table + (size_t)(s0 + at) * a.c.max_pages;
-        const int mask16 = (1 << (a.c.shift - 4)) - 1;
-        int entries = -1, page[2] = {-1, -1};
-        const auto look_up = [&](int step) {     // the pages of step `step`, -1 where there is none
-            if ((step & 31) == 0) {
-                const int64_t key = (int64_t)key0 + (int64_t)(step + (int)lane / 2) * kStride + (lane & 1) * 16;
-                entries = key < sq.length ? table[key >> a.c.shift] : -1;
-                if (entries >= a.c.pages) entries = -1;
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) page[h] = step < steps ? __builtin_amdgcn_readlane(entries, (step & 31) * 2 + h) : -1;
+        const uint32_t mask16 = (1u << (a.c.shift - 4)) - 1;
+        uint32_t where_lo = kNoPage, where_hi = 0;
+        struct Ahead {
+            Codes<NB> k[2], v[2];
+            uint32_t lo[2], hi[2];
         };
-        const auto load = [&](const uint8_t* cache, int step, Codes<NB> (&x)[2]) {
+        Ahead ahead[kDepth];
+        const auto look_up = [&](int step, Ahead& x) {
+            if ((step & 31) == 0 && step < steps) {
+                const int64_t key = (int64_t)key0 + (int64_t)(step + (int)lane / 2) * kStride + (lane & 1) * 16;
+                const int entry = key < sq.length ? table[key >> a.c.shift] : -1;
+                const uint64_t w = group_at<NB>(a.c, entry, head, (uint32_t)(key >> 4) & mask16);
+                where_lo = (uint32_t)w;
+                where_hi = (uint32_t)(w >> 32);
+            }
+            const int l = (step < steps ? step & 31 : (steps - 1) & 31) * 2;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const uint32_t k16 = (uint32_t)((key0 + step * kStride) / 16 + h) & mask16;
-                const Rsrc r = span_rsrc(cache, stream_at(a.c, page[h] < 0 ? 0 : page[h], head), page[h] < 0 ? 0 : a.c.head_bytes);
-                load_codes<NB>(r, k16, i, g, x[h]);
+                x.lo[h] = __builtin_amdgcn_readlane(where_lo, l + h);
+                x.hi[h] = __builtin_amdgcn_readlane(where_hi, l + h);
             }
         };
-        Codes<NB> xk[2], xv[2];
-        if (steps > 0) {
-            look_up(0);
-            load(a.c.k, 0, xk);
-            load(a.c.v, 0, xv);
-        }
-        for (int step = 0; step < steps; ++step) {
+        const auto load = [&](const uint8_t* cache, const Ahead& x, Codes<NB> (&c)[2]) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) load_codes<NB>(cache, (uint64_t)x.hi[h] << 32 | x.lo[h], i, g, c[h]);
+        };
+        const auto one_step = [&](int step, Ahead& x) {
             const int key = key0 + step * kStride;
-            const bool there[2] = {page[0] >= 0, page[1] >= 0};
+            const bool there[2] = {(x.lo[0] & kNoPage) == 0, (x.lo[1] & kNoPage) == 0};
             const bool full = there[0] && there[1] && key >= all_lo && key + 32 <= all_hi;
             f32x4 score[QT][2];
 #pragma unroll
@@ -480,14 +493,14 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
             for (int s = 0; s < NB; ++s)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const u32x4 fk = decode8(xk[h].w[s], scale_of<NB>(xk[h], M::piece(s), i, g));
+                    const u32x4 fk = decode8(x.k[h].w[s], scale_of<NB>(x.k[h], M::piece(s), i, g));
 #pragma unroll
                     for (int t = 0; t < QT; ++t)
 #pragma unroll
                         for (int p = 0; p < P; ++p) score[t][h] = mfma<false>(fk, fq[t][s][p], score[t][h]);
                 }
-            look_up(step + 1);
-            load(a.c.k, step + 1, xk);
+            look_up(step + kDepth, x);
+            load(a.c.k, x, x.k);
             bool odd = false;                     // values that may not be finite where some row does not see them
             if (!full) {
 #pragma unroll
@@ -495,11 +508,11 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
                     const int mine_key = key + 16 * h + (int)i;
                     const bool in = there[h] && mine_key >= any_lo && mine_key < any_hi;
 #pragma unroll
-                    for (int s = 0; s < NB; ++s) xv[h].w[s] = in ? xv[h].w[s] : 0;
+                    for (int s = 0; s < NB; ++s) x.v[h].w[s] = in ? x.v[h].w[s] : 0;
 #pragma unroll
                     for (int p = 0; p < M::kPieces; ++p) {
-                        xv[h].s[p] = in ? xv[h].s[p] : 0x7F7F7F7F;
-                        odd |= scale_byte<NB>(xv[h], p, i, g) >= 253;
+                        x.v[h].s[p] = in ? x.v[h].s[p] : 0x7F7F7F7F;
+                        odd |= scale_byte<NB>(x.v[h], p, i, g) >= 253;
                     }
                 }
                 odd = __builtin_amdgcn_ballot_w64(odd) != 0;
@@ -509,12 +522,12 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
 #pragma unroll
                 for (int s = 0; s < NB; ++s)
                     *reinterpret_cast<u32x4*>(mine + value_at<NB>(16 * h + i, M::unit(s, g))) =
-                        decode8(xv[h].w[s], scale_of<NB>(xv[h], M::piece(s), i, g));
+                        decode8(x.v[h].w[s], scale_of<NB>(x.v[h], M::piece(s), i, g));
             wave_fence();
-            load(a.c.v, step + 1, xv);
+            load(a.c.v, x, x.v);
             // the first values are read while the weights are formed
             const uint8_t* const column = mine + value_at<NB>(4 * g + i / 4, i % 4 / 2) + i % 2 * 8;
-            constexpr int kAhead = ND < 8 ? ND : 8;
+            constexpr int kAhead = 4;
             u32x4 fv[kAhead];
 #pragma unroll
             for (int d = 0; d < kAhead; ++d) fv[d] = load_columns(column + 32 * d, 16 * kValueRow<NB>);
@@ -555,7 +568,7 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
             for (int t = 0; t < QT; ++t) {
                 cut_weights<P>(p[t], fp[t]);
 #pragma unroll
-                for (int x = 0; x < P; ++x) sum[t] = mfma<false>(u32x4{0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80}, fp[t][x], sum[t]);
+                for (int y = 0; y < P; ++y) sum[t] = mfma<false>(u32x4{0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80}, fp[t][y], sum[t]);
             }
             if (!odd) {
 #pragma unroll
@@ -587,6 +600,27 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
                 }
             }
             wave_fence();
+        };
+        if (steps > 0) {
+#pragma unroll
+            for (int y = 0; y < kDepth; ++y) {
+                look_up(y, ahead[y]);
+                load(a.c.k, ahead[y], ahead[y].k);
+                __builtin_amdgcn_sched_barrier(0);               // in the order of the loop, whose waits count them
+                load(a.c.v, ahead[y], ahead[y].v);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        // (no way leads past one of a turn's steps into the next turn: waits for loads count those of the steps between)
+        int step = 0;
+        if constexpr (kDepth == 2) {
+            for (; step + 1 < steps; step += 2) {
+                one_step(step, ahead[0]);
+                one_step(step + 1, ahead[1]);
+            }
+            if (step < steps) one_step(step, ahead[0]);
+        } else {
+            for (; step < steps; ++step) one_step(step, ahead[0]);
         }
 
         const bool whole = u0 == 0 && n == units;
@@ -656,48 +690,76 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
 }
 
 // Joins the parts of a tile that begins in workgroup blockIdx.x and is cut,
-// blockIdx.y's rows of it.  The lanes of D / 4 values take the parts in turn, so
-// that few rows of many parts wait for memory once.
-constexpr int kJoinRows = 4;                     // workgroups in y
+// blockIdx.y's rows of it.  D / 4 lanes have a row, or, where a tile lies in many
+// parts (few rows of a long sequence), every S-th part of one row.
 template <int DT, int NB, int QT, Share SH>
 __global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttention a, const float* work, unsigned groups)
 {
     constexpr int D = 32 * NB, R = kTileRows<QT, SH>, L = D / 4, S = 256 / L;
     __shared__ f32x4 sums[S][L];
-    __shared__ float maxima[4], weights[S];
+    __shared__ float maxima[S], weights[S];
     const Cut cut = reinterpret_cast<const Cut*>(work)[blockIdx.x];
     if (cut.tokens == 0) return;
     const int tid = threadIdx.x, stripe = tid / L, at = tid % L, group = a.heads / a.c.kv_heads;
     const int rows = rows_of(cut.tokens, group, cut.tile, R), count = cut.last - (int)blockIdx.x + 1;
-    const auto part = [&](int x) { return part_of<D, R>(const_cast<float*>(work), groups, 2 * (blockIdx.x + x) + (x == 0 ? 1 : 0)); };
-    for (int r = blockIdx.y; r < rows; r += kJoinRows) {
-        float m = -__builtin_inff();
-        for (int x = tid; x < count; x += 256) m = fmaxf(m, part(x)[R * D + r]);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
-        if (tid % 64 == 0) maxima[tid / 64] = m;
-        __syncthreads();
-        m = fmaxf(fmaxf(maxima[0], maxima[1]), fmaxf(maxima[2], maxima[3]));
-        float l = 0.0f;
+    const bool many = count > 4;
+    for (int r0 = many ? (int)blockIdx.y : (int)blockIdx.y * S; r0 < rows; r0 += many ? (int)gridDim.y : (int)gridDim.y * S) {
+        const int r = many ? r0 : r0 + stripe;
+        float m = -__builtin_inff(), l = 0.0f;
         f32x4 v = {0, 0, 0, 0};
-        if (stripe < S) {
-#pragma unroll 4
-            for (int x = stripe; x < count; x += S) {
-                const float* p = part(x);
-                const float f = under(p[R * D + r], m);
-                l += p[R * D + R + r] * f;
-                v += *reinterpret_cast<const f32x4*>(p + r * D + at * 4) * f;
-            }
-            sums[stripe][at] = v;
-            if (at == 0) weights[stripe] = l;
-        }
-        __syncthreads();
-        if (stripe == 0) {
+        if (stripe < S && r < rows) {            // running, as the parts themselves were formed; four parts asked for at once
+            for (int x = many ? stripe : 0; x < count; x += many ? 4 * S : 4) {
+                float pm[4], pl[4];
+                f32x4 pv[4];
 #pragma unroll
-            for (int x = 1; x < S; ++x) { v += sums[x][at]; l += weights[x]; }
-            write_values<DT>(a, out_row(cut.row0, group, a.heads, cut.head, (uint32_t)cut.tile * R + r), D, at * 4, v, m, l);
+                for (int y = 0; y < 4; ++y) {
+                    const int z = x + y * (many ? S : 1);
+                    pm[y] = -__builtin_inff();
+                    pl[y] = 0.0f;
+                    pv[y] = f32x4{0, 0, 0, 0};
+                    if (z < count) {
+                        const float* p = part_of<D, R>(const_cast<float*>(work), groups, 2 * (blockIdx.x + z) + (z == 0 ? 1 : 0));
+                        pm[y] = p[R * D + r];
+                        pl[y] = p[R * D + R + r];
+                        pv[y] = *reinterpret_cast<const f32x4*>(p + r * D + at * 4);
+                    }
+                }
+                const float most = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m), old = under(m, most);
+                l *= old;
+                v *= old;
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const float f = under(pm[y], most);
+                    l += pl[y] * f;
+                    v += pv[y] * f;
+                }
+                m = most;
+            }
         }
-        __syncthreads();
+        if (many) {
+            if (stripe < S) {
+                sums[stripe][at] = v;
+                if (at == 0) { maxima[stripe] = m; weights[stripe] = l; }
+            }
+            __syncthreads();
+            if (stripe == 0) {
+                float most = m;
+#pragma unroll
+                for (int x = 1; x < S; ++x) most = fmaxf(most, maxima[x]);
+                l *= under(m, most);
+                v *= under(m, most);
+#pragma unroll
+                for (int x = 1; x < S; ++x) {
+                    const float f = under(maxima[x], most);
+                    v += sums[x][at] * f;
+                    l += weights[x] * f;
+                }
+                m = most;
+            }
+            __syncthreads();
+        }
+        if (many ? stripe == 0 : stripe < S && r < rows)
+            write_values<DT>(a, out_row(cut.row0, group, a.heads, cut.head, (uint32_t)cut.tile * R + r), D, at * 4, v, m, l);
     }
 }
 
@@ -716,7 +778,7 @@ hipError_t attention_launch(const CacheAttention& a, float* work, size_t least, 
     attention_kernel<DT, NB, QT, SH><<<W, 64 * kRowWaves, 0, st>>>(a, work, (uint32_t)least, (uint32_t)(most < 0x7FFFFFFF ? most : 0x7FFFFFFF));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attention_join_kernel<DT, NB, QT, SH><<<dim3(W, kJoinRows), 256, 0, st>>>(a, work, W);
+    attention_join_kernel<DT, NB, QT, SH><<<dim3(W, 4), 256, 0, st>>>(a, work, W);
     return hipGetLastError();
 }
 
