@@ -11,7 +11,7 @@ hipError_t launch_attention_fp32(int d, const CacheAttention& a, size_t rows, hi
 size_t cache_attention_work(size_t tokens, size_t heads, size_t kv_heads, size_t d)
 {
     const size_t rows = tokens > 0x7FFFFFFF ? tokens : tokens * (heads / kv_heads);
-    const size_t b = attention_work_t<kBF16>((int)d, rows), h = attention_work_t<kF16>((int)d, rows), f = attention_work_t<kF32>((int)d, rows);
+    const size_t b = attention_work_t<kBF16>((int)d, rows, kv_heads), h = attention_work_t<kF16>((int)d, rows, kv_heads), f = attention_work_t<kF32>((int)d, rows, kv_heads);
     return b > h ? (b > f ? b : f) : h > f ? h : f;
 }
 

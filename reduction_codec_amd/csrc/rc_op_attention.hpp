@@ -165,11 +165,14 @@ __device__ __forceinline__ void wave_fence()
 // many as its rows see; the first tile of a causal sequence sees the fewest and
 // the last the most, so tile j and the j-th from the end go together as a pair,
 // and all pairs of a sequence count alike (a pair may end in units that stand
-// for nothing).  All units of all pairs of all heads of all sequences stand in one
-// row, and workgroup w of W takes the w-th part of them, so that sequences of all
-// lengths load the card alike.  A tile that is cut is joined by a second kernel: a
-// workgroup leaves at most two parts, of the tile that it takes over (slot 2 w)
-// and of the one that it leaves (slot 2 w + 1).
+// for nothing).  All units of all pairs of all sequences stand in one row, which
+// is cut into ranges of one length, so that sequences of all lengths load the card
+// alike, and a workgroup takes a range of one head.  The workgroups of the heads
+// of a range run side by side: what they read of a page lies together (64 long
+// sequences, bf16, heads of 128: 4.6 TB/s where heads followed one another, TBD
+// so).  A tile that is cut is joined by a second kernel: a workgroup leaves at most
+// two parts, of the tile that it takes over (slot 2 w) and of the one that it
+// leaves (slot 2 w + 1).
 struct Sequence {
     int row0, tokens, length;                    // first row of q; rows; tokens in the cache
 };
@@ -237,8 +240,8 @@ __device__ __forceinline__ Sequence sequence(const CacheAttention& a, int s, uin
 
 // What a workgroup leaves of a cut tile: where it starts, for the joining kernel.
 struct Cut {
-    int32_t row0, tokens, tile, head;            // of the tile; tokens = 0: none begins here
-    int32_t last, pad[3];                        // the last workgroup that has a part of it
+    int32_t row0, tokens, tile;                  // of the tile; tokens = 0: none begins here
+    int32_t parts;                               // in this and the next ranges of the head
 };
 
 // The workspace: W cuts, then 2 W parts of R rows: D sums each, then R maxima, R sums of weights.
@@ -314,12 +317,14 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
     const uint32_t group = a.heads / a.c.kv_heads;
     const int kv = a.c.kv_heads;
-    // the workgroups of an XCD, every eighth, take neighbouring parts: they share keys and values in its cache
-    const unsigned groups = gridDim.x, worker = blockIdx.x % 8 * (groups / 8) + blockIdx.x / 8;
+    // the workgroups of an XCD, every eighth, take neighbouring ranges: they share lines, and tiles of rows what they see
+    const unsigned groups = gridDim.x, xcd = blockIdx.x % 8, left = groups % 8;
+    const unsigned worker = xcd * (groups / 8) + (xcd < left ? xcd : left) + blockIdx.x / 8;
+    const int range = worker / kv, head = worker % kv, most_ranges = groups / kv;
 
     const auto units_of = [&](const Sequence& q) {
         const Tiles t = tiles_of<R>(a, q, group);
-        return t.units * t.pairs * kv;
+        return t.units * t.pairs;
     };
     // sequences s0 .. to LDS, and their units' sum
     const auto look = [&](int s0) -> int64_t {
@@ -358,12 +363,12 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
 #pragma unroll
         for (int w = 0; w < kRowWaves; ++w) total += sums[w];
     }
-    const int64_t workers = total < groups ? total : groups;
+    const int64_t ranges = total < most_ranges ? total : most_ranges;
     Cut* const cuts = reinterpret_cast<Cut*>(work);
-    if (tid == 0) cuts[worker] = Cut{0, 0, 0, 0, 0, {0, 0, 0}};
-    if (worker >= workers) return;
-    int64_t pos = total * worker / workers;
-    const int64_t end = total * (worker + 1) / workers;
+    if (tid == 0) cuts[worker] = Cut{0, 0, 0, 0};
+    if (range >= ranges) return;
+    int64_t pos = total * range / ranges;
+    const int64_t end = total * (range + 1) / ranges;
     int s0 = 0;
     uint8_t* const mine = values[wave];
 
@@ -378,9 +383,7 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
                              __builtin_amdgcn_readfirstlane(seqs[at].length)};
         const Tiles tl = tiles_of<R>(a, sq, group);
         const int64_t rel = pos - base - before[at], item = rel / tl.units, v = rel - item * tl.units;
-        const int head = __builtin_amdgcn_readfirstlane((int)(item / tl.pairs));
-        int tile = __builtin_amdgcn_readfirstlane((int)(item - (int64_t)head * tl.pairs));     // of a pair, the later one first
-        tile = tl.tiles - 1 - tile;
+        int tile = tl.tiles - 1 - (int)item;     // of a pair, the later one first
         Extent ex = extent<R>(a, sq, group, tile);
         int64_t u = v;
         if (u >= ex.units) {
@@ -683,7 +686,7 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
         }
         if (u0 == 0 && !whole && tid == 0) {
             const int64_t last = pos + units - 1;                    // the tile's last unit
-            cuts[worker] = Cut{sq.row0, sq.tokens, tile, head, (int)(((last + 1) * workers - 1) / total), {0, 0, 0}};
+            cuts[worker] = Cut{sq.row0, sq.tokens, tile, (int)(((last + 1) * ranges - 1) / total) - range + 1};
         }
         pos += n;
     }
@@ -701,7 +704,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttentio
     const Cut cut = reinterpret_cast<const Cut*>(work)[blockIdx.x];
     if (cut.tokens == 0) return;
     const int tid = threadIdx.x, stripe = tid / L, at = tid % L, group = a.heads / a.c.kv_heads;
-    const int rows = rows_of(cut.tokens, group, cut.tile, R), count = cut.last - (int)blockIdx.x + 1;
+    const int rows = rows_of(cut.tokens, group, cut.tile, R), count = cut.parts, kv = a.c.kv_heads, head = blockIdx.x % kv;
     const bool many = count > 4;
     for (int r0 = many ? (int)blockIdx.y : (int)blockIdx.y * S; r0 < rows; r0 += many ? (int)gridDim.y : (int)gridDim.y * S) {
         const int r = many ? r0 : r0 + stripe;
@@ -718,7 +721,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttentio
                     pl[y] = 0.0f;
                     pv[y] = f32x4{0, 0, 0, 0};
                     if (z < count) {
-                        const float* p = part_of<D, R>(const_cast<float*>(work), groups, 2 * (blockIdx.x + z) + (z == 0 ? 1 : 0));
+                        const float* p = part_of<D, R>(const_cast<float*>(work), groups, 2 * (blockIdx.x + z * kv) + (z == 0 ? 1 : 0));
                         pm[y] = p[R * D + r];
                         pl[y] = p[R * D + R + r];
                         pv[y] = *reinterpret_cast<const f32x4*>(p + r * D + at * 4);
@@ -759,26 +762,35 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttentio
             __syncthreads();
         }
         if (many ? stripe == 0 : stripe < S && r < rows)
-            write_values<DT>(a, out_row(cut.row0, group, a.heads, cut.head, (uint32_t)cut.tile * R + r), D, at * 4, v, m, l);
+            write_values<DT>(a, out_row(cut.row0, group, a.heads, head, (uint32_t)cut.tile * R + r), D, at * 4, v, m, l);
     }
 }
 
-// Workgroups of a launch, and its workspace.
-template <int DT, int NB, int QT> constexpr unsigned kGroups = 256 * row_groups(Terms<DT>::v, NB, QT);
-template <int DT, int NB, int QT, Share SH>
-constexpr size_t attention_bytes()
+// Workgroups of a launch: whole ranges of all heads; and its workspace.
+template <int DT, int NB, int QT>
+constexpr unsigned attention_groups(size_t kv)
 {
-    return kGroups<DT, NB, QT> * (sizeof(Cut) + 2 * kTileRows<QT, SH> * (32 * NB + 2) * sizeof(float));
+    const unsigned fit = 256 * row_groups(Terms<DT>::v, NB, QT), heads = (unsigned)kv;
+    return heads < fit ? fit / heads * heads : heads;
+}
+template <int DT, int NB, int QT, Share SH>
+constexpr size_t attention_bytes(size_t kv)
+{
+    return attention_groups<DT, NB, QT>(kv) * (sizeof(Cut) + 2 * kTileRows<QT, SH> * (32 * NB + 2) * sizeof(float));
 }
 
 template <int DT, int NB, int QT, Share SH>
 hipError_t attention_launch(const CacheAttention& a, float* work, size_t least, size_t most, hipStream_t st)
 {
-    constexpr unsigned W = kGroups<DT, NB, QT>;
-    attention_kernel<DT, NB, QT, SH><<<W, 64 * kRowWaves, 0, st>>>(a, work, (uint32_t)least, (uint32_t)(most < 0x7FFFFFFF ? most : 0x7FFFFFFF));
+    // no more ranges than units that there can be
+    const size_t kv = a.c.kv_heads, units = ((size_t)a.c.max_pages << a.c.shift) / kUnit + 1;
+    const size_t tiles = ((size_t)a.c.tokens * (a.heads / kv) + kTileRows<QT, SH> - 1) / kTileRows<QT, SH> + a.c.seqs;
+    const size_t W = attention_groups<DT, NB, QT>(kv), need = units < W && tiles < W ? units * tiles * kv : W;
+    const unsigned groups = (unsigned)(need < W ? need : W);
+    attention_kernel<DT, NB, QT, SH><<<groups, 64 * kRowWaves, 0, st>>>(a, work, (uint32_t)least, (uint32_t)(most < 0x7FFFFFFF ? most : 0x7FFFFFFF));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attention_join_kernel<DT, NB, QT, SH><<<dim3(W, 4), 256, 0, st>>>(a, work, W);
+    attention_join_kernel<DT, NB, QT, SH><<<dim3(groups, 4), 256, 0, st>>>(a, work, groups);
     return hipGetLastError();
 }
 
@@ -794,17 +806,17 @@ hipError_t attention_d(const CacheAttention& a, size_t rows, hipStream_t st)
     if (a.c.seqs == 1) return attention_launch<DT, NB, 2, Share::kRows>(a, a.work, 0, ~(size_t)0, st);
     const hipError_t e = attention_launch<DT, NB, 2, Share::kRows>(a, a.work, kFewRows, ~(size_t)0, st);
     if (e != hipSuccess) return e;
-    return attention_launch<DT, NB, 2, Share::kTokens>(a, a.work + attention_bytes<DT, NB, 2, Share::kRows>() / 4, 0, kFewRows, st);
+    return attention_launch<DT, NB, 2, Share::kTokens>(a, a.work + attention_bytes<DT, NB, 2, Share::kRows>(a.c.kv_heads) / 4, 0, kFewRows, st);
 }
 
 template <int DT, int NB>
-size_t attention_work_d(size_t rows)
+size_t attention_work_d(size_t rows, size_t kv)
 {
-    const size_t few = attention_bytes<DT, NB, 1, Share::kTokens>(), some = attention_bytes<DT, NB, 2, Share::kTokens>();
+    const size_t few = attention_bytes<DT, NB, 1, Share::kTokens>(kv), some = attention_bytes<DT, NB, 2, Share::kTokens>(kv);
     if (rows <= 16) return few;
     // a hint may ask for the kernel of 16 rows all the same
     if (rows <= kFewRows) return some > few ? some : few;
-    const size_t many = attention_bytes<DT, NB, 2, Share::kRows>() + some;
+    const size_t many = attention_bytes<DT, NB, 2, Share::kRows>(kv) + some;
     return many > few ? many : few;
 }
 
@@ -821,14 +833,14 @@ hipError_t attention_t(int d, const CacheAttention& a, size_t rows, hipStream_t 
 }
 
 template <int DT>
-size_t attention_work_t(int d, size_t rows)
+size_t attention_work_t(int d, size_t rows, size_t kv)
 {
     switch (d) {
-    case 64: return attention_work_d<DT, 2>(rows);
-    case 96: return attention_work_d<DT, 3>(rows);
-    case 128: return attention_work_d<DT, 4>(rows);
-    case 192: return attention_work_d<DT, 6>(rows);
-    case 256: return attention_work_d<DT, 8>(rows);
+    case 64: return attention_work_d<DT, 2>(rows, kv);
+    case 96: return attention_work_d<DT, 3>(rows, kv);
+    case 128: return attention_work_d<DT, 4>(rows, kv);
+    case 192: return attention_work_d<DT, 6>(rows, kv);
+    case 256: return attention_work_d<DT, 8>(rows, kv);
     default: return 0;
     }
 }
