@@ -55,28 +55,27 @@ struct RowMap {
     }
 };
 
-// A lane's part of sixteen tokens' codes, and words that hold its scales (a
-// byte's load would be widened as soon as it is there, and so waited for).
+// ---- 32 tokens' codes
+//
+// They are asked for in the order of memory, a lane a block (16 bytes, kLoads
+// times): lanes that took their words as the matrix instructions want them, 64
+// bytes apart, would touch four times the lines (64 long sequences, bf16, heads of
+// 128: 87 us for loads from the first cache alone).  Keys are handed to the lanes
+// that multiply them through LDS, as they are; values pass through LDS anyway.
+// Scales come as words that hold them (a byte's load would be widened as soon as
+// it is there, and so waited for): of keys for the lane that multiplies, of
+// values for the lane that has the block.
+template <int NB> constexpr int kLoads = (NB + 1) / 2;
+template <int NB> constexpr bool kHalves = NB % 4 == 0;  // sixteen tokens are whole tiles, and each sixteen may have a page of its own
+
 template <int NB>
 struct Codes {
-    uint32_t w[NB], s[RowMap<NB>::kPieces];
+    u32x4 w[kLoads<NB>];
 };
 
-// The scale byte of piece p, and the scale.
-template <int NB>
-__device__ __forceinline__ uint32_t scale_byte(const Codes<NB>& c, int p, uint32_t i, uint32_t g)
-{
-    return __builtin_amdgcn_ubfe(c.s[p], (i * NB + RowMap<NB>::block(p, g)) % 4 * 8, 8);
-}
-template <int NB>
-__device__ __forceinline__ float scale_of(const Codes<NB>& c, int p, uint32_t i, uint32_t g)
-{
-    return __uint_as_float(scale_byte<NB>(c, p, i, g) << 23);
-}
-
 // Where sixteen tokens' codes lie in the cache: the byte of the tile that they
-// begin in, and, below its 16, how many sixteens of blocks into it (of 96 and 192
-// values sixteen tokens are no whole tiles) and whether there is no such page.
+// begin in, and, below its 16, how many sixteens of blocks into it (of 64, 96 and
+// 192 values sixteen tokens are no whole tiles) and whether there is no such page.
 constexpr uint32_t kNoPage = 4;
 template <int NB>
 __device__ __forceinline__ uint64_t group_at(const Cache& c, int page, int head, uint32_t k16)
@@ -85,38 +84,61 @@ __device__ __forceinline__ uint64_t group_at(const Cache& c, int page, int head,
     const uint32_t b0 = 16 * NB * k16;
     return stream_at(c, page, head) + b0 / 64 * kMxTile + b0 % 64 / 16;
 }
+__device__ __forceinline__ const uint8_t* tile_at(const uint8_t* cache, uint64_t where) { return cache + (where & ~(uint64_t)15); }
+__device__ __forceinline__ uint32_t block_in(uint64_t where) { return ((uint32_t)where & 3) * 16; }
 
-// Asks for them; lane (i, g) has token i of the sixteen.
+// Lane's block of load j, among the 32 NB of the tokens (a lane beyond them has its first again).
 template <int NB>
-__device__ __forceinline__ void load_codes(const uint8_t* cache, uint64_t where, uint32_t i, uint32_t g, Codes<NB>& c)
+__device__ __forceinline__ uint32_t block_of(int j, uint32_t lane)
 {
-    typedef RowMap<NB> M;
-    constexpr bool kWhole = NB % 4 == 0, kPart = 64 % (16 * NB) == 0;        // whole tiles; a part of one, or (NB = 3, 6) of two
-    const uint32_t rem = kWhole ? 0 : ((uint32_t)where & 3) * 16;
-    const uint8_t* const tile = cache + (where & ~(uint64_t)15);
+    const uint32_t b = 64 * j + lane;
+    return b < 32 * NB ? b : lane;
+}
+
+// The tile and the block in it of load j's block b: the tokens of a page lie
+// together, from its first sixteen on; where tiles are whole each sixteen counts for itself.
+template <int NB>
+struct Spot {
+    const uint8_t* tile;
+    uint32_t block;
+};
+template <int NB>
+__device__ __forceinline__ Spot<NB> spot_of(const uint8_t* cache, const uint64_t (&where)[2], int j, uint32_t b)
+{
+    if constexpr (kHalves<NB>) return {tile_at(cache, where[j / (NB / 4)]), b - j / (NB / 4) * (16 * NB)};
+    else return {tile_at(cache, where[0]), block_in(where[0]) + b};
+}
+
+template <int NB>
+__device__ __forceinline__ void load_codes(const uint8_t* cache, const uint64_t (&where)[2], uint32_t lane, Codes<NB>& c)
+{
 #pragma unroll
-    for (int p = 0; p < M::kPieces; ++p) {
-        const uint32_t b = i * NB + M::block(p, g), r = kWhole || kPart ? b : rem + b;
-        const uint8_t* const at = tile + (kPart ? rem * 16 : 0) + (codes_at(r) + M::byte(p, g));
-        if (M::words(p) == 4) {
-            const u32x4 v = *reinterpret_cast<const u32x4*>(at);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) c.w[(M::first(p) + e) % NB] = v[e];
-        } else if (M::words(p) == 2) {
-            const u32x2 v = *reinterpret_cast<const u32x2*>(at);
-            c.w[M::first(p)] = v.x;
-            c.w[(M::first(p) + 1) % NB] = v.y;
-        } else {
-            c.w[M::first(p)] = *reinterpret_cast<const uint32_t*>(at);
-        }
-        c.s[p] = *reinterpret_cast<const uint32_t*>(tile + (kPart ? rem : 0) + (scale_at(r) & ~3u));
+    for (int j = 0; j < kLoads<NB>; ++j) {
+        const Spot<NB> p = spot_of<NB>(cache, where, j, block_of<NB>(j, lane));
+        c.w[j] = *reinterpret_cast<const u32x4*>(p.tile + codes_at(p.block));
     }
 }
 
-// ---- values in LDS: rows of D bfloat16 values, one a token, 32 bytes apart:
-// the lanes of a store (eight tokens, one 16-byte unit) and of a transposing
-// load (eight tokens, two units) then fall on all banks, D / 8 + 2 units being
-// 2, 10 or 14 modulo 16.
+// The word that holds the scale of block b of a tile's stream, and the scale in it.
+__device__ __forceinline__ uint32_t load_scale(const uint8_t* tile, uint32_t b) { return *reinterpret_cast<const uint32_t*>(tile + (scale_at(b) & ~3u)); }
+__device__ __forceinline__ uint32_t scale_byte(uint32_t word, uint32_t b) { return __builtin_amdgcn_ubfe(word, b % 4 * 8, 8); }
+__device__ __forceinline__ float scale_of(uint32_t word, uint32_t b) { return __uint_as_float(scale_byte(word, b) << 23); }
+
+// Keys' codes in LDS: a token's blocks, and an odd number of 16-byte units from
+// one token to the next, so that eight tokens' fall on all banks.
+template <int NB> constexpr uint32_t kKeyRow = (NB | 1) * 16;
+
+// ---- values in LDS: rows of D bfloat16 values, one a token, 32 bytes apart: the
+// sixteen lanes of a step of a transposing load (four tokens, two 16-byte units)
+// then fall on all banks (D / 8 + 2 units are 2 modulo 8, or 6).  So do the eight
+// lanes of a step of a store, of one or more tokens' blocks (four units each),
+// if neighbouring pairs of blocks begin with different units of their four.
+template <int NB>
+__device__ __forceinline__ u32x4 turned(u32x4 w, uint32_t by)
+{
+    if (NB > 4) w = by & 2 ? u32x4{w.z, w.w, w.x, w.y} : w;
+    return by & 1 ? u32x4{w.y, w.z, w.w, w.x} : w;
+}
 template <int NB> constexpr uint32_t kValueRow = NB * 64 + 32;
 template <int NB>
 __device__ __forceinline__ uint32_t value_at(uint32_t token, uint32_t unit)
@@ -462,8 +484,9 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
         const uint32_t mask16 = (1u << (a.c.shift - 4)) - 1;
         uint32_t where_lo = kNoPage, where_hi = 0;
         struct Ahead {
-            Codes<NB> k[2], v[2];
-            uint32_t lo[2], hi[2];
+            Codes<NB> k, v;
+            uint32_t ks[2][M::kPieces], vs[kLoads<NB>];
+            uint64_t where[2];
         };
         Ahead ahead[kDepth];
         const auto look_up = [&](int step, Ahead& x) {
@@ -476,19 +499,64 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
             }
             const int l = (step < steps ? step & 31 : (steps - 1) & 31) * 2;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                x.lo[h] = __builtin_amdgcn_readlane(where_lo, l + h);
-                x.hi[h] = __builtin_amdgcn_readlane(where_hi, l + h);
-            }
+            for (int h = 0; h < 2; ++h)
+                x.where[h] = (uint64_t)(uint32_t)__builtin_amdgcn_readlane(where_hi, l + h) << 32 | (uint32_t)__builtin_amdgcn_readlane(where_lo, l + h);
         };
-        const auto load = [&](const uint8_t* cache, const Ahead& x, Codes<NB> (&c)[2]) {
+        const auto load_keys = [&](Ahead& x) {
+            load_codes<NB>(a.c.k, x.where, lane, x.k);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) load_codes<NB>(cache, (uint64_t)x.hi[h] << 32 | x.lo[h], i, g, c[h]);
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int p = 0; p < M::kPieces; ++p) {
+                    const uint32_t b = i * NB + M::block(p, g);
+                    x.ks[h][p] = kHalves<NB> ? load_scale(tile_at(a.c.k, x.where[h]), b)
+                                             : load_scale(tile_at(a.c.k, x.where[0]), block_in(x.where[0]) + h * (16 * NB) + b);
+                }
+        };
+        const auto load_values = [&](Ahead& x) {
+            load_codes<NB>(a.c.v, x.where, lane, x.v);
+#pragma unroll
+            for (int j = 0; j < kLoads<NB>; ++j) {
+                const Spot<NB> p = spot_of<NB>(a.c.v, x.where, j, block_of<NB>(j, lane));
+                x.vs[j] = load_scale(p.tile, p.block);
+            }
         };
         const auto one_step = [&](int step, Ahead& x) {
             const int key = key0 + step * kStride;
-            const bool there[2] = {(x.lo[0] & kNoPage) == 0, (x.lo[1] & kNoPage) == 0};
+            const bool there[2] = {(x.where[0] & kNoPage) == 0, (x.where[1] & kNoPage) == 0};
             const bool full = there[0] && there[1] && key >= all_lo && key + 32 <= all_hi;
+#pragma unroll
+            for (int j = 0; j < kLoads<NB>; ++j) {
+                const uint32_t b = block_of<NB>(j, lane);
+                if (NB % 2 == 0 || j + 1 < kLoads<NB> || lane < 32)
+                    *reinterpret_cast<u32x4*>(mine + b / NB * kKeyRow<NB> + b % NB * 16) = x.k.w[j];
+            }
+            wave_fence();
+            uint32_t kw[2][NB];                  // this lane's words of tokens i and 16 + i
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int p = 0; p < M::kPieces; ++p) {
+                    const uint8_t* const at_k = mine + (16 * h + i) * kKeyRow<NB> + M::block(p, g) * 16 + M::byte(p, g);
+                    if (M::words(p) == 4) {
+                        const u32x4 v = *reinterpret_cast<const u32x4*>(at_k);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) kw[h][(M::first(p) + e) % NB] = v[e];
+                    } else if (M::words(p) == 2) {
+                        const u32x2 v = *reinterpret_cast<const u32x2*>(at_k);
+                        kw[h][M::first(p)] = v.x;
+                        kw[h][(M::first(p) + 1) % NB] = v.y;
+                    } else {
+                        kw[h][M::first(p)] = *reinterpret_cast<const uint32_t*>(at_k);
+                    }
+                }
+            float kscale[2][M::kPieces];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int p = 0; p < M::kPieces; ++p) kscale[h][p] = scale_of(x.ks[h][p], i * NB + M::block(p, g));
+            look_up(step + kDepth, x);
+            load_keys(x);
             f32x4 score[QT][2];
 #pragma unroll
             for (int t = 0; t < 2 * QT; ++t) score[t / 2][t % 2] = f32x4{0, 0, 0, 0};
@@ -496,38 +564,40 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
             for (int s = 0; s < NB; ++s)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const u32x4 fk = decode8(x.k[h].w[s], scale_of<NB>(x.k[h], M::piece(s), i, g));
+                    const u32x4 fk = decode8(kw[h][s], kscale[h][M::piece(s)]);
 #pragma unroll
                     for (int t = 0; t < QT; ++t)
 #pragma unroll
                         for (int p = 0; p < P; ++p) score[t][h] = mfma<false>(fk, fq[t][s][p], score[t][h]);
                 }
-            look_up(step + kDepth, x);
-            load(a.c.k, x, x.k);
-            bool odd = false;                     // values that may not be finite where some row does not see them
+            wave_fence();
+            bool odd = false;                    // values that may not be finite where some row does not see them
             if (!full) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int mine_key = key + 16 * h + (int)i;
-                    const bool in = there[h] && mine_key >= any_lo && mine_key < any_hi;
+                for (int j = 0; j < kLoads<NB>; ++j) {
+                    const uint32_t b = block_of<NB>(j, lane), k = b / NB;
+                    const bool in = (k < 16 ? there[0] : there[1]) && key + (int)k >= any_lo && key + (int)k < any_hi;
 #pragma unroll
-                    for (int s = 0; s < NB; ++s) x.v[h].w[s] = in ? x.v[h].w[s] : 0;
-#pragma unroll
-                    for (int p = 0; p < M::kPieces; ++p) {
-                        x.v[h].s[p] = in ? x.v[h].s[p] : 0x7F7F7F7F;
-                        odd |= scale_byte<NB>(x.v[h], p, i, g) >= 253;
-                    }
+                    for (int e = 0; e < 4; ++e) x.v.w[j][e] = in ? x.v.w[j][e] : 0;
+                    x.vs[j] = in ? x.vs[j] : 0x7F7F7F7F;
+                    odd |= scale_byte(x.vs[j], b) >= 253;
                 }
                 odd = __builtin_amdgcn_ballot_w64(odd) != 0;
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int j = 0; j < kLoads<NB>; ++j) {
+                const uint32_t b = block_of<NB>(j, lane);
+                const float scale = scale_of(x.vs[j], b);
+                uint8_t* const at_v = mine + value_at<NB>(b / NB, b % NB * 4);
+                const uint32_t turn = NB == 2 ? b & 1 : b % NB / 2;
+                const u32x4 w = turned<NB>(x.v.w[j], turn);
+                if (NB % 2 == 0 || j + 1 < kLoads<NB> || lane < 32) {
 #pragma unroll
-                for (int s = 0; s < NB; ++s)
-                    *reinterpret_cast<u32x4*>(mine + value_at<NB>(16 * h + i, M::unit(s, g))) =
-                        decode8(x.v[h].w[s], scale_of<NB>(x.v[h], M::piece(s), i, g));
+                    for (int e = 0; e < 4; ++e) *reinterpret_cast<u32x4*>(at_v + ((e + turn) & 3) * 16) = decode8(w[e], scale);
+                }
+            }
             wave_fence();
-            load(a.c.v, x, x.v);
+            load_values(x);
             // the first values are read while the weights are formed
             const uint8_t* const column = mine + value_at<NB>(4 * g + i / 4, i % 4 / 2) + i % 2 * 8;
             constexpr int kAhead = 4;
@@ -608,9 +678,9 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
 #pragma unroll
             for (int y = 0; y < kDepth; ++y) {
                 look_up(y, ahead[y]);
-                load(a.c.k, ahead[y], ahead[y].k);
+                load_keys(ahead[y]);
                 __builtin_amdgcn_sched_barrier(0);               // in the order of the loop, whose waits count them
-                load(a.c.v, ahead[y], ahead[y].v);
+                load_values(ahead[y]);
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
