@@ -365,8 +365,9 @@ rc_status rc_mxfp4_cache_read(const rc_cache *cache, size_t tokens, rc_dtype t, 
  * only, else RC_ERR_UNSUPPORTED) j > p - window.  out: dense, of type t; lse:
  * tokens x heads fp32 values, or NULL.  A row that sees nothing, or only scores of
  * minus infinity, gets out = 0 and lse = -infinity.  What the cache holds where a
- * row does not see does not reach the row, whatever its bytes are; what is not
- * finite where it sees makes its values not finite.
+ * row does not see does not reach the row, whatever its bytes are; a value that is
+ * not finite where it sees makes the row's values of that block of 32 not finite, a
+ * score that is not makes all of them so.
  * Scores and sums are FP32.  Rounding: the weights exp(s_j - max) are multiplied as
  * bfloat16 (t bf16, relative 2^-9), or as two (fp16) or three (fp32) terms of it
  * that hold 16 and 24 bits, and below 2^-126 may count as zero; fp32 queries count as the nearest multiple of 2^-133.

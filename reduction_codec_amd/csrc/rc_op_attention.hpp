@@ -124,6 +124,15 @@ __device__ __forceinline__ uint32_t load_scale(const uint8_t* tile, uint32_t b) 
 __device__ __forceinline__ uint32_t scale_byte(uint32_t word, uint32_t b) { return __builtin_amdgcn_ubfe(word, b % 4 * 8, 8); }
 __device__ __forceinline__ float scale_of(uint32_t word, uint32_t b) { return __uint_as_float(scale_byte(word, b) << 23); }
 
+// Whether a block of four words and this scale has values that binary32 does not
+// hold: all of NaN, 2 and more under 2^127, 4 and more under 2^126 (bit 2 of a code
+// says 2 or more, with bit 1 4 or more).
+__device__ __forceinline__ bool not_finite(u32x4 w, uint32_t scale)
+{
+    const uint32_t two = w.x | w.y | w.z | w.w, four = (w.x & w.x << 1) | (w.y & w.y << 1) | (w.z & w.z << 1) | (w.w & w.w << 1);
+    return scale >= 253 && (scale == 255 || ((scale == 254 ? two : four) & 0x44444444u) != 0);
+}
+
 // Keys' codes in LDS: a token's blocks, and an odd number of 16-byte units from
 // one token to the next, so that eight tokens' fall on all banks.
 template <int NB> constexpr uint32_t kKeyRow = (NB | 1) * 16;
@@ -459,10 +468,12 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
         f32x4 acc[QT][ND];
         f32x4 sum[QT];                           // the weights' sum, four times: a product with ones
         float top[QT];                           // the running maximum in binary logarithms
+        uint32_t marks[QT];                      // blocks that the row sees not finite
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             top[t] = -__builtin_inff();
             sum[t] = f32x4{0, 0, 0, 0};
+            marks[t] = 0;
 #pragma unroll
             for (int d = 0; d < ND; ++d) acc[t][d] = f32x4{0, 0, 0, 0};
         }
@@ -523,6 +534,9 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
         };
         const auto one_step = [&](int step, Ahead& x) {
             const int key = key0 + step * kStride;
+            uint32_t lane = threadIdx.x & 63;    // addresses are formed from it in every step: kept, they would fill registers
+            asm volatile("" : "+v"(lane));
+            const uint32_t i = lane & 15, g = lane >> 4;
             const bool there[2] = {(x.where[0] & kNoPage) == 0, (x.where[1] & kNoPage) == 0};
             const bool full = there[0] && there[1] && key >= all_lo && key + 32 <= all_hi;
 #pragma unroll
@@ -571,18 +585,23 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
                         for (int p = 0; p < P; ++p) score[t][h] = mfma<false>(fk, fq[t][s][p], score[t][h]);
                 }
             wave_fence();
-            bool odd = false;                    // values that may not be finite where some row does not see them
             if (!full) {
 #pragma unroll
                 for (int j = 0; j < kLoads<NB>; ++j) {
+                    // what no row sees counts as zeros; so does a block that is not finite, which would reach the rows
+                    // whose weight for it is zero: the rows that see it are marked
                     const uint32_t b = block_of<NB>(j, lane), k = b / NB;
                     const bool in = (k < 16 ? there[0] : there[1]) && key + (int)k >= any_lo && key + (int)k < any_hi;
+                    const bool wrong = in && not_finite(x.v.w[j], scale_byte(x.vs[j], b));
+                    for (uint64_t left = __builtin_amdgcn_ballot_w64(wrong); left != 0; left &= left - 1) {
+                        const int at_b = (int)block_of<NB>(j, __builtin_ctzll(left)), k_b = key + at_b / NB;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x.v.w[j][e] = in ? x.v.w[j][e] : 0;
-                    x.vs[j] = in ? x.vs[j] : 0x7F7F7F7F;
-                    odd |= scale_byte(x.vs[j], b) >= 253;
+                        for (int t = 0; t < QT; ++t) marks[t] |= k_b >= see_lo[t] && k_b < see_hi[t] ? 1u << at_b % NB : 0;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x.v.w[j][e] = in && !wrong ? x.v.w[j][e] : 0;
+                    x.vs[j] = in && !wrong ? x.vs[j] : 0x7F7F7F7F;
                 }
-                odd = __builtin_amdgcn_ballot_w64(odd) != 0;
             }
 #pragma unroll
             for (int j = 0; j < kLoads<NB>; ++j) {
@@ -643,34 +662,13 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
 #pragma unroll
                 for (int y = 0; y < P; ++y) sum[t] = mfma<false>(u32x4{0x3F803F80, 0x3F803F80, 0x3F803F80, 0x3F803F80}, fp[t][y], sum[t]);
             }
-            if (!odd) {
 #pragma unroll
-                for (int d = 0; d < ND; ++d) {
+            for (int d = 0; d < ND; ++d) {
 #pragma unroll
-                    for (int t = 0; t < QT; ++t)
+                for (int t = 0; t < QT; ++t)
 #pragma unroll
-                        for (int p = 0; p < P; ++p) acc[t][d] = mfma<false>(fv[d % kAhead], fp[t][p], acc[t][d]);
-                    if (d + kAhead < ND) fv[d % kAhead] = load_columns(column + 32 * (d + kAhead), 16 * kValueRow<NB>);
-                }
-            } else {                              // token by token, for the rows that see it alone
-#pragma unroll 1
-                for (int k = 0; k < 32; ++k) {
-                    const uint32_t keep = (int)g != k % 16 / 4 ? 0 : k % 2 ? 0xFFFF0000u : 0x0000FFFFu;
-#pragma unroll
-                    for (int d = 0; d < ND; ++d) {
-                        u32x4 f1 = load_columns(column + 32 * d, 16 * kValueRow<NB>);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) f1[e] &= e == k / 16 * 2 + k % 4 / 2 ? keep : 0;
-#pragma unroll
-                        for (int t = 0; t < QT; ++t) {
-                            f32x4 one = {0, 0, 0, 0};
-#pragma unroll
-                            for (int p = 0; p < P; ++p) one = mfma<false>(f1, fp[t][p], one);
-                            const bool in = key + k >= see_lo[t] && key + k < see_hi[t];
-                            acc[t][d] = in ? acc[t][d] + one : acc[t][d];
-                        }
-                    }
-                }
+                    for (int p = 0; p < P; ++p) acc[t][d] = mfma<false>(fv[d % kAhead], fp[t][p], acc[t][d]);
+                if (d + kAhead < ND) fv[d % kAhead] = load_columns(column + 32 * (d + kAhead), 16 * kValueRow<NB>);
             }
             wave_fence();
         };
@@ -696,6 +694,12 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
             for (; step < steps; ++step) one_step(step, ahead[0]);
         }
 
+#pragma unroll
+        for (int t = 0; t < QT; ++t)
+            if (__builtin_expect(__builtin_amdgcn_ballot_w64(marks[t] != 0) != 0, 0)) {
+#pragma unroll
+                for (int d = 0; d < ND; ++d) acc[t][d] += marks[t] >> (d / 2) & 1 ? __builtin_nanf("") : 0.0f;
+            }
         const bool whole = u0 == 0 && n == units;
         float* const part = part_of<D, R>(work, groups, 2 * worker + (u0 == 0 ? 1 : 0));
         // row r of 16, values 4 u .. of it: their sum, the maximum and the weights' sum
