@@ -317,12 +317,15 @@ __device__ __forceinline__ float under(float m, float most)
 enum class Share : int { kTokens, kRows };
 template <int QT, Share SH> constexpr int kTileRows = 16 * QT * (SH == Share::kRows ? kRowWaves : 1);
 
-// Workgroups of a compute unit (waves of a SIMD): by the registers that a lane
-// needs (queries, sums, scores, codes, and some), and by LDS.
+// Registers that a lane needs, about: queries, sums, scores, codes, and some.
+constexpr int lane_registers(int terms, int nb, int qt)
+{
+    return qt * (nb * 4 * terms + nb * 8 + 8 + 4 * terms) + (qt == 1 ? 2 : 1) * (nb * 4 + 10) + 60;
+}
+// Workgroups of a compute unit (waves of a SIMD): by them and by LDS.
 constexpr int row_groups(int terms, int nb, int qt)
 {
-    const int regs = qt * (nb * 4 * terms + nb * 8 + 8 + 4 * terms) + nb * 4 + 10 + 60 + (qt == 1 ? nb * 4 + 10 : 0);
-    const int by_regs = regs <= 128 ? 4 : regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
+    const int regs = lane_registers(terms, nb, qt), by_regs = regs <= 128 ? 4 : regs <= 168 ? 3 : regs <= 256 ? 2 : 1;
     const int by_lds = 163840 / (kRowWaves * 32 * (nb * 64 + 32) + 4096);
     return by_regs < by_lds ? by_regs : by_lds;
 }
@@ -338,6 +341,9 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
     constexpr int kSeqs = 128;                   // sequences looked at at a time
     constexpr int kStride = SH == Share::kTokens ? kUnit : 32;       // tokens from a wave's step to its next
     constexpr int kDepth = SH == Share::kTokens && QT == 1 ? 2 : 1;  // steps asked for ahead
+    // kept, addresses would take registers that queries and sums need (16 rows of 256 values: 89 spilled, 24 so), but
+    // where there is room they are better kept (prompts, 32 rows of 128 values: 540 us, 513 so)
+    constexpr bool kTight = lane_registers(P, NB, QT) > 230 && lane_registers(P, NB, QT) <= 256;
     constexpr float kLog2e = 1.44269504f;
     typedef RowMap<NB> M;
     __shared__ __attribute__((aligned(16))) uint8_t values[kRowWaves][32 * kValueRow<NB>];
@@ -534,8 +540,8 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
         };
         const auto one_step = [&](int step, Ahead& x) {
             const int key = key0 + step * kStride;
-            uint32_t lane = threadIdx.x & 63;    // addresses are formed from it in every step: kept, they would fill registers
-            asm volatile("" : "+v"(lane));
+            uint32_t lane = threadIdx.x & 63;
+            if constexpr (kTight) asm volatile("" : "+v"(lane));     // addresses are formed from it in every step
             const uint32_t i = lane & 15, g = lane >> 4;
             const bool there[2] = {(x.where[0] & kNoPage) == 0, (x.where[1] & kNoPage) == 0};
             const bool full = there[0] && there[1] && key >= all_lo && key + 32 <= all_hi;
