@@ -786,8 +786,9 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
 }
 
 // Joins the parts of a tile that begins in workgroup blockIdx.x and is cut,
-// blockIdx.y's rows of it.  D / 4 lanes have a row, or, where a tile lies in many
-// parts (few rows of a long sequence), every S-th part of one row.
+// blockIdx.y's rows of it.  D / 4 lanes ask for four parts of a row at once; a row
+// of more parts has as many such stripes as it needs (few rows of a long sequence
+// lie in many parts), and the rest of the workgroup other rows.
 template <int DT, int NB, int QT, Share SH>
 __global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttention a, const float* work, unsigned groups)
 {
@@ -796,65 +797,64 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttentio
     __shared__ float maxima[S], weights[S];
     const Cut cut = reinterpret_cast<const Cut*>(work)[blockIdx.x];
     if (cut.tokens == 0) return;
-    const int tid = threadIdx.x, stripe = tid / L, at = tid % L, group = a.heads / a.c.kv_heads;
+    const int tid = threadIdx.x, at = tid % L, group = a.heads / a.c.kv_heads;
     const int rows = rows_of(cut.tokens, group, cut.tile, R), count = cut.parts, kv = a.c.kv_heads, head = blockIdx.x % kv;
-    const bool many = count > 4;
-    for (int r0 = many ? (int)blockIdx.y : (int)blockIdx.y * S; r0 < rows; r0 += many ? (int)gridDim.y : (int)gridDim.y * S) {
-        const int r = many ? r0 : r0 + stripe;
+    const int need = (count + 3) / 4, stripes = need < S ? need : S, at_once = S / stripes;
+    const int own = tid / L / stripes, stripe = tid / L % stripes;
+    for (int r0 = blockIdx.y * at_once; r0 < rows; r0 += gridDim.y * at_once) {
+        const int r = r0 + own;
+        const bool in = own < at_once && r < rows;
         float m = -__builtin_inff(), l = 0.0f;
         f32x4 v = {0, 0, 0, 0};
-        if (stripe < S && r < rows) {            // running, as the parts themselves were formed; four parts asked for at once
-            for (int x = many ? stripe : 0; x < count; x += many ? 4 * S : 4) {
-                float pm[4], pl[4];
-                f32x4 pv[4];
+        for (int x = stripe; in && x < count; x += 4 * stripes) {    // running, as the parts themselves were formed
+            float pm[4], pl[4];
+            f32x4 pv[4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int z = x + y * (many ? S : 1);
-                    pm[y] = -__builtin_inff();
-                    pl[y] = 0.0f;
-                    pv[y] = f32x4{0, 0, 0, 0};
-                    if (z < count) {
-                        const float* p = part_of<D, R>(const_cast<float*>(work), groups, 2 * (blockIdx.x + z * kv) + (z == 0 ? 1 : 0));
-                        pm[y] = p[R * D + r];
-                        pl[y] = p[R * D + R + r];
-                        pv[y] = *reinterpret_cast<const f32x4*>(p + r * D + at * 4);
-                    }
+            for (int y = 0; y < 4; ++y) {
+                const int z = x + y * stripes;
+                pm[y] = -__builtin_inff();
+                pl[y] = 0.0f;
+                pv[y] = f32x4{0, 0, 0, 0};
+                if (z < count) {
+                    const float* p = part_of<D, R>(const_cast<float*>(work), groups, 2 * (blockIdx.x + z * kv) + (z == 0 ? 1 : 0));
+                    pm[y] = p[R * D + r];
+                    pl[y] = p[R * D + R + r];
+                    pv[y] = *reinterpret_cast<const f32x4*>(p + r * D + at * 4);
                 }
-                const float most = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m), old = under(m, most);
-                l *= old;
-                v *= old;
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const float f = under(pm[y], most);
-                    l += pl[y] * f;
-                    v += pv[y] * f;
-                }
-                m = most;
             }
+            const float most = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m), old = under(m, most);
+            l *= old;
+            v *= old;
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const float f = under(pm[y], most);
+                l += pl[y] * f;
+                v += pv[y] * f;
+            }
+            m = most;
         }
-        if (many) {
-            if (stripe < S) {
-                sums[stripe][at] = v;
-                if (at == 0) { maxima[stripe] = m; weights[stripe] = l; }
+        if (stripes > 1) {
+            const int slot = own * stripes + stripe;
+            if (in) {
+                sums[slot][at] = v;
+                if (at == 0) { maxima[slot] = m; weights[slot] = l; }
             }
             __syncthreads();
-            if (stripe == 0) {
+            if (in && stripe == 0) {
                 float most = m;
-#pragma unroll
-                for (int x = 1; x < S; ++x) most = fmaxf(most, maxima[x]);
+                for (int x = 1; x < stripes; ++x) most = fmaxf(most, maxima[slot + x]);
                 l *= under(m, most);
                 v *= under(m, most);
-#pragma unroll
-                for (int x = 1; x < S; ++x) {
-                    const float f = under(maxima[x], most);
-                    v += sums[x][at] * f;
-                    l += weights[x] * f;
+                for (int x = 1; x < stripes; ++x) {
+                    const float f = under(maxima[slot + x], most);
+                    v += sums[slot + x][at] * f;
+                    l += weights[slot + x] * f;
                 }
                 m = most;
             }
             __syncthreads();
         }
-        if (many ? stripe == 0 : stripe < S && r < rows)
+        if (in && stripe == 0)
             write_values<DT>(a, out_row(cut.row0, group, a.heads, head, (uint32_t)cut.tile * R + r), D, at * 4, v, m, l);
     }
 }

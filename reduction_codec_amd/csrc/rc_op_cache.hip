@@ -59,7 +59,116 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v)
 
 constexpr int kAppendLanes = 256;
 
-// One token a workgroup row of the grid; blockIdx.y cuts its heads (q, k, v).
+// The codes of eight values of a block whose largest is 2^(ex + 2) and more.
+__device__ __forceinline__ uint32_t codes8(const double (&y)[8], int ex)
+{
+    uint32_t w = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        w = fp4_enc(w, round_odd(__builtin_ldexp(y[2 * b], -ex)), round_odd(__builtin_ldexp(y[2 * b + 1], -ex)), 1.0f, b);
+    return w;
+}
+
+// Upper halves of binary64 order magnitudes as their exponents do.
+__device__ __forceinline__ uint32_t largest8(const double (&y)[8])
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t m = (uint32_t)(__double_as_longlong(y[e]) >> 32) & 0x7FFFFFFF;
+        top = top > m ? top : m;
+    }
+    return top;
+}
+
+__device__ __forceinline__ int exponent_of(uint32_t top)
+{
+    const int ex = (int)(top >> 20) - 1023 - 2;
+    return ex < -127 ? -127 : ex > 127 ? 127 : ex;
+}
+
+// A lane has two units of eight values of a head that are turned together, and
+// those of every (kAppendLanes / (D / 16))-th head, so that a token's angles are
+// read once: units u and u + rot / 16 of the first rot values (or neighbours if
+// interleaved), neighbours of the rest, and of values.  A block is four units: of
+// neighbouring lanes' first units, or second ones, or both of two lanes.  That
+// takes rot to be a multiple of 64 (or neighbours) and D of 64; what is not goes
+// unit by unit below.  10240 tokens of 48 heads of 128, bf16 (221 MB): TBD us, 89
+// unit by unit, where every head reads the angles and half of it twice.
+template <int DT, int D>
+__global__ __launch_bounds__(kAppendLanes) void cache_append_pairs_kernel(const CacheAppend a)
+{
+    constexpr int I = D / 16, ES = Elem<DT>::size, HP = kAppendLanes / I;
+    const int token = blockIdx.x, kv = a.c.kv_heads, all = a.heads + 2 * kv, item = threadIdx.x % I;
+    const RowPlace at = row_place(a.c, token);
+    if (at.seq < 0 || threadIdx.x >= HP * I) return;
+    const int page = page_of(a.c, at.seq, at.pos), half = a.rot / 2;
+    const bool turned = item * 16 < a.rot, split = turned && !a.interleaved;
+    double cs[8], sn[8];
+    if (turned) {
+        const float* turn = a.rotation + (size_t)(at.pos < 0 ? 0 : at.pos) * a.rot + item * 8;
+        float c[8], s[8];
+        load8<kF32>(reinterpret_cast<const uint8_t*>(turn), c);
+        load8<kF32>(reinterpret_cast<const uint8_t*>(turn + half), s);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) { cs[e] = c[e]; sn[e] = s[e]; }
+    }
+    for (int row = blockIdx.y * HP + threadIdx.x / I; row < all; row += gridDim.y * HP) {
+        const bool query = row < a.heads, value = row >= a.heads + kv, both = split && !value;
+        const int head = row - (query ? 0 : value ? a.heads + kv : a.heads);
+        const uint8_t* src = static_cast<const uint8_t*>(query ? a.q : value ? a.v : a.k) +
+                             ((size_t)token * (query ? a.q_stride : value ? a.v_stride : a.k_stride) + (size_t)head * D) * ES;
+        // the units of this lane
+        const int u0 = both ? item : 2 * item, u1 = both ? item + half / 8 : 2 * item + 1;
+        float v0[8], v1[8];
+        load8<DT>(src + u0 * 8 * ES, v0);
+        load8<DT>(src + u1 * 8 * ES, v1);
+        double y0[8], y1[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) { y0[e] = v0[e]; y1[e] = v1[e]; }
+        if (both) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const double p = y0[e], q = y1[e];
+                y0[e] = p * cs[e] - q * sn[e];
+                y1[e] = q * cs[e] + p * sn[e];
+            }
+        } else if (turned && !value) {           // neighbours
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const double p = y0[2 * e], q = y0[2 * e + 1], r = y1[2 * e], s = y1[2 * e + 1];
+                y0[2 * e] = p * cs[e] - q * sn[e];
+                y0[2 * e + 1] = q * cs[e] + p * sn[e];
+                y1[2 * e] = r * cs[4 + e] - s * sn[4 + e];
+                y1[2 * e + 1] = s * cs[4 + e] + r * sn[4 + e];
+            }
+        }
+        if (query) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v0[e] = DT == kF32 ? (float)y0[e] : round_odd(y0[e]);
+                v1[e] = DT == kF32 ? (float)y1[e] : round_odd(y1[e]);
+            }
+            uint8_t* out = static_cast<uint8_t*>(a.q_out) + ((size_t)token * a.heads + head) * D * ES;
+            store8<DT>(out + u0 * 8 * ES, v0);
+            store8<DT>(out + u1 * 8 * ES, v1);
+            continue;
+        }
+        const uint32_t t0 = largest8(y0), t1 = largest8(y1), t = t0 > t1 ? t0 : t1;
+        const uint32_t other = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)t, 0xB1, 0xF, 0xF, false);     // the lane beside
+        const int ex0 = exponent_of(both ? quad_max(t0) : t > other ? t : other), ex1 = both ? exponent_of(quad_max(t1)) : ex0;
+        const uint32_t w0 = codes8(y0, ex0), w1 = codes8(y1, ex1);
+        if (page < 0) continue;
+        uint8_t* out = (value ? a.c.v : a.c.k) + stream_at(a.c, page, head);
+        const uint32_t block = (uint32_t)(at.pos & ((1 << a.c.shift) - 1)) * (D / 32);
+        *reinterpret_cast<uint32_t*>(out + codes_at(block + u0 / 4) + u0 % 4 * 4) = w0;
+        *reinterpret_cast<uint32_t*>(out + codes_at(block + u1 / 4) + u1 % 4 * 4) = w1;
+        if (u0 % 4 == 0) out[scale_at(block + u0 / 4)] = (uint8_t)(ex0 + 127);
+        if (both && u1 % 4 == 0) out[scale_at(block + u1 / 4)] = (uint8_t)(ex1 + 127);
+    }
+}
+
+// Unit by unit: one token a row of the grid; blockIdx.y cuts its heads (q, k, v).
 template <int DT, int D>
 __global__ __launch_bounds__(kAppendLanes) void cache_append_kernel(const CacheAppend a)
 {
@@ -109,18 +218,8 @@ __global__ __launch_bounds__(kAppendLanes) void cache_append_kernel(const CacheA
         store8<DT>(static_cast<uint8_t*>(a.q_out) + (((size_t)token * a.heads + head) * D + c * 8) * ES, v);
         return;
     }
-    uint32_t top = 0;                            // upper halves order magnitudes as their exponents do
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t m = (uint32_t)(__double_as_longlong(y[e]) >> 32) & 0x7FFFFFFF;
-        top = top > m ? top : m;
-    }
-    int ex = (int)(quad_max(top) >> 20) - 1023 - 2;
-    ex = ex < -127 ? -127 : ex > 127 ? 127 : ex;
-    uint32_t w = 0;
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-        w = fp4_enc(w, round_odd(__builtin_ldexp(y[2 * b], -ex)), round_odd(__builtin_ldexp(y[2 * b + 1], -ex)), 1.0f, b);
+    const int ex = exponent_of(quad_max(largest8(y)));
+    const uint32_t w = codes8(y, ex);
     const int page = page_of(a.c, at.seq, at.pos);
     if (page < 0) return;
     uint8_t* out = (value ? a.c.v : a.c.k) + stream_at(a.c, page, head);
@@ -158,6 +257,15 @@ __global__ __launch_bounds__(kAppendLanes) void cache_read_kernel(const Cache c,
 template <int DT, int D>
 hipError_t append_t(const CacheAppend& a, hipStream_t st)
 {
+    if constexpr (D % 64 == 0) {
+        if (a.rot % 64 == 0 || a.interleaved) {
+            // few tokens: their heads side by side
+            constexpr unsigned HP = kAppendLanes / (D / 16);
+            const unsigned turns = ((unsigned)(a.heads + 2 * a.c.kv_heads) + HP - 1) / HP, y = a.c.tokens < 2048 ? turns : 1;
+            cache_append_pairs_kernel<DT, D><<<dim3((unsigned)a.c.tokens, y), kAppendLanes, 0, st>>>(a);
+            return hipGetLastError();
+        }
+    }
     const unsigned y = ((unsigned)(a.heads + 2 * a.c.kv_heads) * (D / 8) + kAppendLanes - 1) / kAppendLanes;
     cache_append_kernel<DT, D><<<dim3((unsigned)a.c.tokens, y), kAppendLanes, 0, st>>>(a);
     return hipGetLastError();
