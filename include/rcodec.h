@@ -308,7 +308,7 @@ rc_status rc_grad_norm_clip(const rc_grad *grads, size_t count, float scale, flo
  * offsets[s] <= i < offsets[s + 1] of what a call takes are the sequence's last
  * tokens: row i stands at position lengths[s] - offsets[s + 1] + i.
  * table, lengths and offsets are device arrays, read by the kernels (a captured
- * graph follows them), and what they hold cannot lead outside the buffers:
+ * graph follows them) and left alone while a call runs; what they hold cannot lead outside the buffers:
  * lengths count as at least 0 and at most max_pages * page, offsets are clamped to
  * the rows there are, and pages outside [0, pages) hold no token.
  * Offsets that do not ascend give unspecified results.  Rows that belong to no
@@ -369,12 +369,12 @@ rc_status rc_mxfp4_cache_read(const rc_cache *cache, size_t tokens, rc_dtype t, 
  * not finite where it sees makes the row's values of that block of 32 not finite, a
  * score that is not makes all of them so.
  * Scores and sums are FP32.  Rounding: the weights exp(s_j - max) are multiplied as
- * bfloat16 (t bf16, relative 2^-9), or as two (fp16) or three (fp32) terms of it
+ * bfloat16 (t bf16, relative 2^-8), or as two (fp16) or three (fp32) terms of it
  * that hold 16 and 24 bits, and below 2^-126 may count as zero; fp32 queries count as the nearest multiple of 2^-133.
  * max_query: no sequence has more rows than this, 0 if not known: a hint that the
  * choice of kernels goes by, results are right whatever it says.
- * workspace: rc_mxfp4_cache_attention_workspace(heads, d) bytes, 16-byte aligned,
- * written before it is read, for one call at a time.  Calls repeat bit for bit. */
+ * workspace: rc_mxfp4_cache_attention_workspace(tokens, heads, kv_heads, d) bytes,
+ * 16-byte aligned, written before it is read, for one call at a time.  Calls repeat bit for bit. */
 size_t rc_mxfp4_cache_attention_workspace(size_t tokens, size_t heads, size_t kv_heads, size_t d);
 rc_status rc_mxfp4_cache_attention(const rc_cache *cache, rc_dtype t, size_t tokens, size_t heads, const void *q,
                                    size_t q_stride, float scale, int causal, size_t window, size_t max_query,

@@ -15,7 +15,7 @@
 // the cache.  What an E2M1 code under an E8M0 scale stands for is a bfloat16, so
 // keys and values are decoded exactly; queries are cut into one (bf16), two
 // (fp16) or three (fp32) bfloat16 terms that add up to them, and so are the
-// weights exp(s_j - m): one term rounds them to 2^-9 of themselves, which is
+// weights exp(s_j - m): one term rounds them to 2^-8 of themselves, which is
 // less than what rounding the result to bfloat16 costs, as its errors average out.
 #pragma once
 
@@ -163,7 +163,7 @@ __device__ __forceinline__ float max_of_row(float v)
     const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
-// Weights of 2 x 4 tokens as P bfloat16 terms that add up to them (to 2^-9,
+// Weights of 2 x 4 tokens as P bfloat16 terms that add up to them (to 2^-8,
 // 2^-17 and 2^-24 of themselves).
 template <int P>
 __device__ __forceinline__ void cut_weights(const float (&p)[8], u32x4 (&t)[P])
@@ -410,7 +410,12 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
     uint8_t* const mine = values[wave];
 
     while (pos < end) {
-        while (pos >= base + here) { base += here; s0 += kSeqs; here = look(s0); }
+        while (pos >= base + here) {
+            base += here;
+            s0 += kSeqs;
+            if (s0 >= a.c.seqs) return;          // lengths that changed since they were summed up
+            here = look(s0);
+        }
         int at = 0;                              // the last sequence that begins at or before pos
 #pragma unroll
         for (int step = kSeqs / 2; step > 0; step /= 2)

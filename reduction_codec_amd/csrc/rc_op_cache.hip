@@ -133,6 +133,16 @@ __device__ __forceinline__ int exponent_of(uint32_t top)
     return ex < -127 ? -127 : ex > 127 ? 127 : ex;
 }
 
+// The token of a workgroup, and a grid of `y` workgroups for each: a grid's x is
+// at most 2^32 lanes, so z takes what is more.
+constexpr unsigned kTokensOfX = 1u << 22;
+__device__ __forceinline__ unsigned token_of_block() { return blockIdx.z * gridDim.x + blockIdx.x; }
+dim3 grid_of_tokens(int tokens, unsigned y)
+{
+    const unsigned n = (unsigned)tokens, x = n < kTokensOfX ? n : kTokensOfX;
+    return dim3(x, y, (n + x - 1) / x);
+}
+
 // A lane has two units of eight values of a head that are turned together, and
 // those of every (kTokenLanes / (D / 16))-th head, so that a token's angles are
 // read once: units u and u + rot / 16 of the first rot values (or neighbours if
@@ -149,7 +159,8 @@ template <int DT, int D>
 __global__ __launch_bounds__(kTokenLanes) void cache_append_pairs_kernel(const CacheAppend a)
 {
     constexpr int I = D / 16, ES = Elem<DT>::size, HP = kTokenLanes / I;
-    const int token = blockIdx.x, kv = a.c.kv_heads, all = a.heads + 2 * kv, item = threadIdx.x % I;
+    const int token = (int)token_of_block(), kv = a.c.kv_heads, all = a.heads + 2 * kv, item = threadIdx.x % I;
+    if ((unsigned)token >= (unsigned)a.c.tokens) return;
     const RowPlace at = row_place(a.c, token);
     if (at.seq < 0 || threadIdx.x >= HP * I) return;
     const int page = page_of(a.c, at.seq, at.pos), half = a.rot / 2;
@@ -220,9 +231,10 @@ template <int DT, int D>
 __global__ __launch_bounds__(kAppendLanes) void cache_append_kernel(const CacheAppend a)
 {
     constexpr int U = D / 8, ES = Elem<DT>::size;
-    const int token = blockIdx.x, kv = a.c.kv_heads, unit = blockIdx.y * kAppendLanes + threadIdx.x;
+    const int token = (int)token_of_block(), kv = a.c.kv_heads, unit = blockIdx.y * kAppendLanes + threadIdx.x;
     int head = unit / U;
     const int c = unit % U;
+    if ((unsigned)token >= (unsigned)a.c.tokens) return;
     const RowPlace at = row_place(a.c, token);
     if (at.seq < 0 || head >= a.heads + 2 * kv) return;
     const bool query = head < a.heads, value = head >= a.heads + kv;
@@ -278,7 +290,8 @@ template <int DT, int D>
 __global__ __launch_bounds__(kTokenLanes) void cache_read_kernel(const Cache c, void* k, void* v)
 {
     constexpr int U = D / 8, ES = Elem<DT>::size;
-    const int token = blockIdx.x, units = 2 * U * c.kv_heads;
+    const int token = (int)token_of_block(), units = 2 * U * c.kv_heads;
+    if ((unsigned)token >= (unsigned)c.tokens) return;
     const RowPlace at = row_place(c, token);
     if (at.seq < 0) return;
     const int page = page_of(c, at.seq, at.pos);
@@ -311,12 +324,12 @@ hipError_t append_t(const CacheAppend& a, hipStream_t st)
             // few tokens: their heads side by side
             constexpr unsigned HP = kTokenLanes / (D / 16);
             const unsigned turns = ((unsigned)(a.heads + 2 * a.c.kv_heads) + HP - 1) / HP, y = a.c.tokens < kFewTokens ? turns : 1;
-            cache_append_pairs_kernel<DT, D><<<dim3((unsigned)a.c.tokens, y), kTokenLanes, 0, st>>>(a);
+            cache_append_pairs_kernel<DT, D><<<grid_of_tokens(a.c.tokens, y), kTokenLanes, 0, st>>>(a);
             return hipGetLastError();
         }
     }
     const unsigned y = ((unsigned)(a.heads + 2 * a.c.kv_heads) * (D / 8) + kAppendLanes - 1) / kAppendLanes;
-    cache_append_kernel<DT, D><<<dim3((unsigned)a.c.tokens, y), kAppendLanes, 0, st>>>(a);
+    cache_append_kernel<DT, D><<<grid_of_tokens(a.c.tokens, y), kAppendLanes, 0, st>>>(a);
     return hipGetLastError();
 }
 
@@ -324,7 +337,7 @@ template <int DT, int D>
 hipError_t read_t(const Cache& c, void* k, void* v, hipStream_t st)
 {
     const unsigned turns = ((unsigned)c.kv_heads * 2 * (D / 8) + kTokenLanes - 1) / kTokenLanes, y = c.tokens < kFewTokens ? turns : 1;
-    cache_read_kernel<DT, D><<<dim3((unsigned)c.tokens, y), kTokenLanes, 0, st>>>(c, k, v);
+    cache_read_kernel<DT, D><<<grid_of_tokens(c.tokens, y), kTokenLanes, 0, st>>>(c, k, v);
     return hipGetLastError();
 }
 
