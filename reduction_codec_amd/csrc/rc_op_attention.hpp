@@ -276,8 +276,8 @@ struct Cut {
 };
 
 // The workspace: W cuts, then 2 W parts of R rows: D sums each, then R maxima, R sums of weights.
-template <int D, int R>
-__device__ __forceinline__ float* part_of(float* work, unsigned groups, unsigned slot)
+template <int D>
+__device__ __forceinline__ float* part_of(float* work, unsigned groups, int R, unsigned slot)
 {
     return work + (size_t)groups * (sizeof(Cut) / 4) + (size_t)slot * (R * (D + 2));
 }
@@ -725,7 +725,7 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
                 for (int d = 0; d < ND; ++d) acc[t][d] += marks[t] >> (d / 2) & 1 ? __builtin_nanf("") : 0.0f;
             }
         const bool whole = u0 == 0 && n == units;
-        float* const part = part_of<D, R>(work, groups, 2 * worker + (u0 == 0 ? 1 : 0));
+        float* const part = part_of<D>(work, groups, R, 2 * worker + (u0 == 0 ? 1 : 0));
         // row r of 16, values 4 u .. of it: their sum, the maximum and the weights' sum
         const auto put = [&](int r, int u, f32x4 x, float m, float l) {
             if (whole) {
@@ -790,20 +790,33 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
     }
 }
 
-// Joins the parts of a tile that begins in workgroup blockIdx.x and is cut,
-// blockIdx.y's rows of it.  D / 4 lanes ask for four parts of a row at once; a row
-// of more parts has as many such stripes as it needs (few rows of a long sequence
-// lie in many parts), and the rest of the workgroup other rows.
-template <int DT, int NB, int QT, Share SH>
-__global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttention a, const float* work, unsigned groups)
+// What a launch of the kernel above leaves: its workspace, workgroups, and rows of a tile.
+struct Parts {
+    float* work;
+    unsigned groups;
+    int rows;
+};
+
+// Joins the parts of a tile that begins in workgroup blockIdx.x of the first
+// launch, or of the second, and is cut, blockIdx.y's rows of it.  D / 4 lanes ask
+// for four parts of a row at once; a row of more parts has as many such stripes as
+// it needs (few rows of a long sequence lie in many parts), and the rest of the
+// workgroup other rows.  One kernel for both launches: chunks of up to 37
+// fp32 rows of five sequences take 57 us with two, 53 so.
+template <int DT, int NB>
+__global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttention a, const Parts first, const Parts second)
 {
-    constexpr int D = 32 * NB, R = kTileRows<QT, SH>, L = D / 4, S = 256 / L;
+    constexpr int D = 32 * NB, L = D / 4, S = 256 / L;
     __shared__ f32x4 sums[S][L];
     __shared__ float maxima[S], weights[S];
-    const Cut cut = reinterpret_cast<const Cut*>(work)[blockIdx.x];
+    const bool later = blockIdx.x >= first.groups;
+    const float* const work = later ? second.work : first.work;
+    const unsigned groups = later ? second.groups : first.groups, worker = blockIdx.x - (later ? first.groups : 0);
+    const int R = later ? second.rows : first.rows;
+    const Cut cut = reinterpret_cast<const Cut*>(work)[worker];
     if (cut.tokens == 0) return;
     const int tid = threadIdx.x, at = tid % L, group = a.heads / a.c.kv_heads;
-    const int rows = rows_of(cut.tokens, group, cut.tile, R), count = cut.parts, kv = a.c.kv_heads, head = blockIdx.x % kv;
+    const int rows = rows_of(cut.tokens, group, cut.tile, R), count = cut.parts, kv = a.c.kv_heads, head = worker % kv;
     const int need = (count + 3) / 4, stripes = need < S ? need : S, at_once = S / stripes;
     const int own = tid / L / stripes, stripe = tid / L % stripes;
     for (int r0 = blockIdx.y * at_once; r0 < rows; r0 += gridDim.y * at_once) {
@@ -821,7 +834,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttentio
                 pl[y] = 0.0f;
                 pv[y] = f32x4{0, 0, 0, 0};
                 if (z < count) {
-                    const float* p = part_of<D, R>(const_cast<float*>(work), groups, 2 * (blockIdx.x + z * kv) + (z == 0 ? 1 : 0));
+                    const float* p = part_of<D>(const_cast<float*>(work), groups, R, 2 * (worker + z * kv) + (z == 0 ? 1 : 0));
                     pm[y] = p[R * D + r];
                     pl[y] = p[R * D + R + r];
                     pv[y] = *reinterpret_cast<const f32x4*>(p + r * D + at * 4);
@@ -878,17 +891,14 @@ constexpr size_t attention_bytes(size_t kv)
 }
 
 template <int DT, int NB, int QT, Share SH>
-hipError_t attention_launch(const CacheAttention& a, float* work, size_t least, size_t most, hipStream_t st)
+hipError_t attention_launch(const CacheAttention& a, float* work, size_t least, size_t most, Parts& parts, hipStream_t st)
 {
     // no more ranges than units that there can be
     const size_t kv = a.c.kv_heads, units = ((size_t)a.c.max_pages << a.c.shift) / kUnit + 1;
     const size_t tiles = ((size_t)a.c.tokens * (a.heads / kv) + kTileRows<QT, SH> - 1) / kTileRows<QT, SH> + a.c.seqs;
     const size_t W = attention_groups<DT, NB, QT>(kv), need = units < W && tiles < W ? units * tiles * kv : W;
-    const unsigned groups = (unsigned)(need < W ? need : W);
-    attention_kernel<DT, NB, QT, SH><<<groups, 64 * kRowWaves, 0, st>>>(a, work, (uint32_t)least, (uint32_t)(most < 0x7FFFFFFF ? most : 0x7FFFFFFF));
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    attention_join_kernel<DT, NB, QT, SH><<<dim3(groups, 4), 256, 0, st>>>(a, work, groups);
+    parts = {work, (unsigned)(need < W ? need : W), kTileRows<QT, SH>};
+    attention_kernel<DT, NB, QT, SH><<<parts.groups, 64 * kRowWaves, 0, st>>>(a, work, (uint32_t)least, (uint32_t)(most < 0x7FFFFFFF ? most : 0x7FFFFFFF));
     return hipGetLastError();
 }
 
@@ -899,12 +909,21 @@ constexpr size_t kFewRows = 32;
 template <int DT, int NB>
 hipError_t attention_d(const CacheAttention& a, size_t rows, hipStream_t st)
 {
-    if (rows <= 16) return attention_launch<DT, NB, 1, Share::kTokens>(a, a.work, 0, ~(size_t)0, st);
-    if (rows <= kFewRows) return attention_launch<DT, NB, 2, Share::kTokens>(a, a.work, 0, ~(size_t)0, st);
-    if (a.c.seqs == 1) return attention_launch<DT, NB, 2, Share::kRows>(a, a.work, 0, ~(size_t)0, st);
-    const hipError_t e = attention_launch<DT, NB, 2, Share::kRows>(a, a.work, kFewRows, ~(size_t)0, st);
+    const size_t all = ~(size_t)0;
+    Parts first = {}, second = {};
+    hipError_t e;
+    if (rows <= 16) e = attention_launch<DT, NB, 1, Share::kTokens>(a, a.work, 0, all, first, st);
+    else if (rows <= kFewRows) e = attention_launch<DT, NB, 2, Share::kTokens>(a, a.work, 0, all, first, st);
+    else if (a.c.seqs == 1) e = attention_launch<DT, NB, 2, Share::kRows>(a, a.work, 0, all, first, st);
+    else {
+        e = attention_launch<DT, NB, 2, Share::kRows>(a, a.work, kFewRows, all, first, st);
+        if (e != hipSuccess) return e;
+        float* const behind = a.work + attention_bytes<DT, NB, 2, Share::kRows>(a.c.kv_heads) / 4;
+        e = attention_launch<DT, NB, 2, Share::kTokens>(a, behind, 0, kFewRows, second, st);
+    }
     if (e != hipSuccess) return e;
-    return attention_launch<DT, NB, 2, Share::kTokens>(a, a.work + attention_bytes<DT, NB, 2, Share::kRows>(a.c.kv_heads) / 4, 0, kFewRows, st);
+    attention_join_kernel<DT, NB><<<dim3(first.groups + second.groups, 4), 256, 0, st>>>(a, first, second);
+    return hipGetLastError();
 }
 
 template <int DT, int NB>
