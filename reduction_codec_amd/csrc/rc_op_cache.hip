@@ -25,14 +25,18 @@ __device__ __forceinline__ float round_odd(double x)
     return __uint_as_float(u);
 }
 
-template <int DT>
+// ONCE: nobody reads them again (past the caches, 12288 tokens are appended in 55
+// us, 59 through them).
+template <int DT, bool ONCE = false>
 __device__ __forceinline__ void load8(const uint8_t* p, float (&v)[8])
 {
+    const u32x4* const at = reinterpret_cast<const u32x4*>(p);
+    const auto load = [&](int i) { return ONCE ? __builtin_nontemporal_load(at + i) : at[i]; };
     if constexpr (DT == kF32) {
-        const u32x4 a = *reinterpret_cast<const u32x4*>(p), b = *reinterpret_cast<const u32x4*>(p + 16);
+        const u32x4 a = load(0), b = load(1);
         for (int e = 0; e < 4; ++e) { v[e] = __uint_as_float(a[e]); v[4 + e] = __uint_as_float(b[e]); }
     } else {
-        widen8<DT>(*reinterpret_cast<const u32x4*>(p), v);
+        widen8<DT>(load(0), v);
     }
 }
 
@@ -58,11 +62,12 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v)
 }
 
 // Lanes of a workgroup where units go one by one, and where it takes a token.
-// Every wave looks its token up, so a token has few: 12288 tokens of 48 heads
-// of 128 in bf16 are appended in 59 us by two waves, 76 by four, 60 by one.  But
-// fewer than kFewTokens tokens leave the card empty, so their heads are cut as
-// well: 64 tokens 3.7 us cut and 5.0 whole, 768 tokens 7.7 and 8.0, 1536 tokens
-// 11.8 and 11.4; read back 2.8 and 3.0, 3.7 and 3.9, 4.8 and 5.2, 12288 16.9 and 15.2.
+// Every wave looks its token up, so a token has few: 12288 tokens of 48 heads of
+// 128 in bf16 are appended in 55 us by two waves (76 by four, 60 by one, against
+// 59, before values were loaded past the caches).  But fewer than kFewTokens
+// tokens leave the card empty, so their heads are cut as well: 64 tokens 3.7 us
+// cut and 5.0 whole, 768 tokens 7.7 and 8.0, 1536 tokens 11.8 and 11.4; read back
+// 2.8 and 3.0, 3.7 and 3.9, 4.8 and 5.2, 12288 16.9 and 15.2.
 constexpr int kAppendLanes = 256, kTokenLanes = 128, kFewTokens = 1024;
 
 // The upper half of |y| with its last bit set where the lower half holds
@@ -149,11 +154,11 @@ dim3 grid_of_tokens(int tokens, unsigned y)
 // interleaved), neighbours of the rest, and of values.  A block is four units: of
 // neighbouring lanes' first units, or second ones, or both of two lanes.  That
 // takes rot to be a multiple of 64 (or neighbours) and D of 64; what is not goes
-// unit by unit below.  12288 tokens of 48 heads of 128, bf16 (265 MB): 59 us, 4.5
+// unit by unit below.  12288 tokens of 48 heads of 128, bf16 (265 MB): 55 us, 4.8
 // TB/s; 89 us unit by unit, where every head reads the angles and half of it
 // twice.  The loads of a token wait for its place and one another, so that the
 // kernel is bound by how many tokens are in flight: values asked for ahead cost
-// registers and with them waves (64 to 67 us), and neighbouring tokens on one XCD,
+// registers and with them waves (64 to 67 us, against 59), and neighbouring tokens on one XCD,
 // whose codes share lines, change nothing.
 template <int DT, int D>
 __global__ __launch_bounds__(kTokenLanes) void cache_append_pairs_kernel(const CacheAppend a)
@@ -182,8 +187,8 @@ __global__ __launch_bounds__(kTokenLanes) void cache_append_pairs_kernel(const C
         // the units of this lane
         const int u0 = both ? item : 2 * item, u1 = both ? item + half / 8 : 2 * item + 1;
         float v0[8], v1[8];
-        load8<DT>(src + u0 * 8 * ES, v0);
-        load8<DT>(src + u1 * 8 * ES, v1);
+        load8<DT, true>(src + u0 * 8 * ES, v0);
+        load8<DT, true>(src + u1 * 8 * ES, v1);
         double y0[8], y1[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) { y0[e] = v0[e]; y1[e] = v1[e]; }
