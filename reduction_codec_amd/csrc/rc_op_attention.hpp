@@ -801,8 +801,7 @@ struct Parts {
 // launch, or of the second, and is cut, blockIdx.y's rows of it.  D / 4 lanes ask
 // for four parts of a row at once; a row of more parts has as many such stripes as
 // it needs (few rows of a long sequence lie in many parts), and the rest of the
-// workgroup other rows.  One kernel for both launches: chunks of up to 37
-// fp32 rows of five sequences take 57 us with two, 53 so.
+// workgroup other rows.  One kernel for both launches: 4 us a call less.
 template <int DT, int NB>
 __global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttention a, const Parts first, const Parts second)
 {
@@ -902,8 +901,13 @@ hipError_t attention_launch(const CacheAttention& a, float* work, size_t least, 
     return hipGetLastError();
 }
 
-// Rows of a sequence up to which the waves share its tokens.
-constexpr size_t kFewRows = 32;
+// Rows of a sequence up to which the waves share its tokens, in tiles of 32 (of 16
+// if there are no more rows: one token of 64 sequences of 16000, 181 us, in tiles
+// of 32 194): tiles of 128 rows leave waves without any, and a batch needs both
+// kernels.  Heads of 128 on a quarter of them, bf16, us sharing tokens and rows: 16
+// sequences of 4000, 32 rows 35 and 52, 64 rows 47 and 62, 128 rows 67 and 75; 4 of
+// 30000, 64 rows 70 and 104, 128 rows 115 and 132.
+constexpr size_t kFewRows = 128;
 
 // `rows`: no sequence has more rows of q a head.
 template <int DT, int NB>
