@@ -371,8 +371,8 @@ rc_status rc_mxfp4_cache_read(const rc_cache *cache, size_t tokens, rc_dtype t, 
  * Scores and sums are FP32.  Rounding: the weights exp(s_j - max) are multiplied as
  * bfloat16 (t bf16, relative 2^-8), or as two (fp16) or three (fp32) terms of it
  * that hold 16 and 24 bits, and below 2^-126 may count as zero; fp32 queries count as the nearest multiple of 2^-133.
- * lse is the logarithm of the sum of the weights so rounded (what out is divided by):
- * off by at most 2^-8 for bf16, 2^-16 for fp16, and FP32's own rounding for fp32.
+ * out is divided by the sum of the weights so rounded; lse is the logarithm of the sum of
+ * the weights before that, FP32 for every type of the queries.
  * max_query: no sequence has more rows than this, 0 if not known: a hint that the
  * choice of kernels goes by, results are right whatever it says.
  * workspace: rc_mxfp4_cache_attention_workspace(tokens, heads, kv_heads, d) bytes,

@@ -163,6 +163,14 @@ __device__ __forceinline__ float max_of_row(float v)
     const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
+// Sum over the four lanes that share a row, in each of them.
+__device__ __forceinline__ float sum_of_row(float v)
+{
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
 // Weights of 2 x 4 tokens as P bfloat16 terms that add up to them (to 2^-8,
 // 2^-17 and 2^-24 of themselves).
 template <int P>
@@ -275,11 +283,12 @@ struct Cut {
     int32_t parts;                               // in this and the next ranges of the head
 };
 
-// The workspace: W cuts, then 2 W parts of R rows: D sums each, then R maxima, R sums of weights.
+// The workspace: W cuts, then 2 W parts of R rows: D sums each, then R maxima, R sums of the weights as they are
+// multiplied and R of the weights themselves.
 template <int D>
 __device__ __forceinline__ float* part_of(float* work, unsigned groups, int R, unsigned slot)
 {
-    return work + (size_t)groups * (sizeof(Cut) / 4) + (size_t)slot * (R * (D + 2));
+    return work + (size_t)groups * (sizeof(Cut) / 4) + (size_t)slot * (R * (D + 3));
 }
 
 // Rows of tile `tile` that there are, and where row r of q is written.
@@ -293,17 +302,24 @@ __device__ __forceinline__ size_t out_row(int row0, uint32_t group, int heads, i
     return (size_t)(row0 + r / group) * heads + head * group + r % group;
 }
 
-// Four values of a row from their sum v, the sum l of the weights and the maximum m.
+// A row's maximum, the sum of its weights as they are multiplied, rounded, which
+// its values are divided by (their errors cancel), and the sum of the weights
+// themselves, which the log-sum-exp is formed of.
+struct Weights {
+    float m, l, exact;
+};
+
+// Four values of a row from their sum v and the row's weights.
 template <int DT>
-__device__ __forceinline__ void write_values(const CacheAttention& a, size_t row, int d, int at, f32x4 v, float m, float l)
+__device__ __forceinline__ void write_values(const CacheAttention& a, size_t row, int d, int at, f32x4 v, const Weights& w)
 {
     constexpr float kLn2 = 0.693147181f;
-    const float f = 1.0f / l;
-    const f32x4 o = l == 0.0f ? f32x4{0, 0, 0, 0} : v * f;
+    const float f = 1.0f / w.l;
+    const f32x4 o = w.l == 0.0f ? f32x4{0, 0, 0, 0} : v * f;
     const size_t i = row * d + at;
     if constexpr (DT == kF32) *reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + i) = o;
     else *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.out) + i) = u32x2{narrow2<DT>(o[0], o[1]), narrow2<DT>(o[2], o[3])};
-    if (a.lse && at == 0) a.lse[row] = l == 0.0f ? -__builtin_inff() : (m + __builtin_log2f(l)) * kLn2;
+    if (a.lse && at == 0) a.lse[row] = w.l == 0.0f ? -__builtin_inff() : (w.m + __builtin_log2f(w.exact)) * kLn2;
 }
 
 // The weight that a part of maximum m has under the maximum `most`.
@@ -345,12 +361,13 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
     // where there is room they are better kept (prompts, 32 rows of 128 values: 540 us, 513 so)
     constexpr bool kTight = lane_registers(P, NB, QT) > 230 && lane_registers(P, NB, QT) <= 256;
     constexpr float kLog2e = 1.44269504f;
+    constexpr bool kExactSum = P < 3;             // three terms are the weight itself
     typedef RowMap<NB> M;
     __shared__ __attribute__((aligned(16))) uint8_t values[kRowWaves][32 * kValueRow<NB>];
     __shared__ int64_t before[kSeqs];            // units before each of them
     __shared__ Sequence seqs[kSeqs];
     __shared__ int64_t sums[kRowWaves];
-    __shared__ float wave_max[kRowWaves][16 * QT], wave_sum[kRowWaves][16 * QT];
+    __shared__ Weights wave_weights[kRowWaves][16 * QT];
     const uint32_t tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), i = lane & 15, g = lane >> 4;
     const uint32_t group = a.heads / a.c.kv_heads;
     const int kv = a.c.kv_heads;
@@ -478,12 +495,14 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
 
         f32x4 acc[QT][ND];
         f32x4 sum[QT];                           // the weights' sum, four times: a product with ones
+        float exact[QT];                         // this lane's weights before they are rounded, if the log-sum-exp is asked for
         float top[QT];                           // the running maximum in binary logarithms
         uint32_t marks[QT];                      // blocks that the row sees not finite
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
             top[t] = -__builtin_inff();
             sum[t] = f32x4{0, 0, 0, 0};
+            exact[t] = 0.0f;
             marks[t] = 0;
 #pragma unroll
             for (int d = 0; d < ND; ++d) acc[t][d] = f32x4{0, 0, 0, 0};
@@ -673,9 +692,15 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
 #pragma unroll
                     for (int d = 0; d < ND; ++d) acc[t][d] *= f;
                     sum[t] *= f;
+                    exact[t] *= f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) p[t][e] = __builtin_amdgcn_exp2f(p[t][e] - base);
                 }
+            }
+            if (kExactSum && a.lse) {            // (prompts of 4500 tokens on average 468 us, 485 with it)
+#pragma unroll
+                for (int t = 0; t < QT; ++t)
+                    exact[t] += ((p[t][0] + p[t][1]) + (p[t][2] + p[t][3])) + ((p[t][4] + p[t][5]) + (p[t][6] + p[t][7]));
             }
             prefer(2);
             u32x4 fp[QT][P];
@@ -727,26 +752,27 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
         const bool whole = u0 == 0 && n == units;
         float* const part = part_of<D>(work, groups, R, 2 * worker + (u0 == 0 ? 1 : 0));
         // row r of 16, values 4 u .. of it: their sum, the maximum and the weights' sum
-        const auto put = [&](int r, int u, f32x4 x, float m, float l) {
+        const auto put = [&](int r, int u, f32x4 x, const Weights& w) {
             if (whole) {
-                write_values<DT>(a, out_row(sq.row0, group, a.heads, head, r0 + r), D, u * 4, x, m, l);
+                write_values<DT>(a, out_row(sq.row0, group, a.heads, head, r0 + r), D, u * 4, x, w);
             } else {
                 *reinterpret_cast<f32x4*>(part + (skip + r) * D + u * 4) = x;
-                if (u == 0) { part[R * D + skip + r] = m; part[R * D + R + skip + r] = l; }
+                if (u == 0) { part[R * D + skip + r] = w.m; part[R * D + R + skip + r] = w.l; part[R * D + 2 * R + skip + r] = w.exact; }
             }
         };
 #pragma unroll
         for (int t = 0; t < QT; ++t) {
-            if (g == 0) { wave_max[wave][16 * t + i] = top[t]; wave_sum[wave][16 * t + i] = sum[t][0]; }
+            const float all = kExactSum ? sum_of_row(exact[t]) : sum[t][0];
+            if (g == 0) wave_weights[wave][16 * t + i] = Weights{top[t], sum[t][0], all};
         }
         float* const o = reinterpret_cast<float*>(mine);             // 16 rows of D sums, 16 bytes apart
         if constexpr (SH == Share::kTokens) {    // the waves' sums meet
             __syncthreads();
 #pragma unroll
             for (int t = 0; t < QT; ++t) {
-                float most = wave_max[0][16 * t + i];
+                float most = wave_weights[0][16 * t + i].m;
 #pragma unroll
-                for (int w = 1; w < kRowWaves; ++w) most = fmaxf(most, wave_max[w][16 * t + i]);
+                for (int w = 1; w < kRowWaves; ++w) most = fmaxf(most, wave_weights[w][16 * t + i].m);
                 const float f = under(top[t], most);
 #pragma unroll
                 for (int d = 0; d < ND; ++d) *reinterpret_cast<f32x4*>(o + i * (D + 4) + 16 * d + 4 * g) = acc[t][d] * f;
@@ -755,15 +781,20 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
                     const int r = e / (D / 4), u = e % (D / 4);
                     if (16 * t + r >= own) continue;
                     f32x4 x = {0, 0, 0, 0};
-                    float m = -__builtin_inff(), l = 0.0f;
+                    Weights all = {-__builtin_inff(), 0.0f, 0.0f};
 #pragma unroll
                     for (int w = 0; w < kRowWaves; ++w) {
                         x += *reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(values[w]) + r * (D + 4) + u * 4);
-                        m = fmaxf(m, wave_max[w][16 * t + r]);
+                        all.m = fmaxf(all.m, wave_weights[w][16 * t + r].m);
                     }
 #pragma unroll
-                    for (int w = 0; w < kRowWaves; ++w) l += wave_sum[w][16 * t + r] * under(wave_max[w][16 * t + r], m);
-                    put(16 * t + r, u, x, m, l);
+                    for (int w = 0; w < kRowWaves; ++w) {
+                        const Weights& one = wave_weights[w][16 * t + r];
+                        const float f = under(one.m, all.m);
+                        all.l += one.l * f;
+                        all.exact += one.exact * f;
+                    }
+                    put(16 * t + r, u, x, all);
                 }
                 __syncthreads();
             }
@@ -776,8 +807,7 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
                 for (int e = lane; e < 16 * (D / 4); e += 64) {
                     const int r = e / (D / 4), u = e % (D / 4);
                     if (16 * t + r < own)
-                        put(16 * t + r, u, *reinterpret_cast<const f32x4*>(o + r * (D + 4) + u * 4), wave_max[wave][16 * t + r],
-                            wave_sum[wave][16 * t + r]);
+                        put(16 * t + r, u, *reinterpret_cast<const f32x4*>(o + r * (D + 4) + u * 4), wave_weights[wave][16 * t + r]);
                 }
                 wave_fence();
             }
@@ -807,7 +837,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttentio
 {
     constexpr int D = 32 * NB, L = D / 4, S = 256 / L;
     __shared__ f32x4 sums[S][L];
-    __shared__ float maxima[S], weights[S];
+    __shared__ Weights weights[S];
     const bool later = blockIdx.x >= first.groups;
     const float* const work = later ? second.work : first.work;
     const unsigned groups = later ? second.groups : first.groups, worker = blockIdx.x - (later ? first.groups : 0);
@@ -821,58 +851,57 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttentio
     for (int r0 = blockIdx.y * at_once; r0 < rows; r0 += gridDim.y * at_once) {
         const int r = r0 + own;
         const bool in = own < at_once && r < rows;
-        float m = -__builtin_inff(), l = 0.0f;
+        Weights w = {-__builtin_inff(), 0.0f, 0.0f};
         f32x4 v = {0, 0, 0, 0};
         for (int x = stripe; in && x < count; x += 4 * stripes) {    // running, as the parts themselves were formed
-            float pm[4], pl[4];
+            Weights pw[4];
             f32x4 pv[4];
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
                 const int z = x + y * stripes;
-                pm[y] = -__builtin_inff();
-                pl[y] = 0.0f;
+                pw[y] = Weights{-__builtin_inff(), 0.0f, 0.0f};
                 pv[y] = f32x4{0, 0, 0, 0};
                 if (z < count) {
                     const float* p = part_of<D>(const_cast<float*>(work), groups, R, 2 * (worker + z * kv) + (z == 0 ? 1 : 0));
-                    pm[y] = p[R * D + r];
-                    pl[y] = p[R * D + R + r];
+                    pw[y] = Weights{p[R * D + r], p[R * D + R + r], p[R * D + 2 * R + r]};
                     pv[y] = *reinterpret_cast<const f32x4*>(p + r * D + at * 4);
                 }
             }
-            const float most = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])), m), old = under(m, most);
-            l *= old;
+            const float most = fmaxf(fmaxf(fmaxf(pw[0].m, pw[1].m), fmaxf(pw[2].m, pw[3].m)), w.m), old = under(w.m, most);
+            w = Weights{most, w.l * old, w.exact * old};
             v *= old;
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-                const float f = under(pm[y], most);
-                l += pl[y] * f;
+                const float f = under(pw[y].m, most);
+                w.l += pw[y].l * f;
+                w.exact += pw[y].exact * f;
                 v += pv[y] * f;
             }
-            m = most;
         }
         if (stripes > 1) {
             const int slot = own * stripes + stripe;
             if (in) {
                 sums[slot][at] = v;
-                if (at == 0) { maxima[slot] = m; weights[slot] = l; }
+                if (at == 0) weights[slot] = w;
             }
             __syncthreads();
             if (in && stripe == 0) {
-                float most = m;
-                for (int x = 1; x < stripes; ++x) most = fmaxf(most, maxima[slot + x]);
-                l *= under(m, most);
-                v *= under(m, most);
+                float most = w.m;
+                for (int x = 1; x < stripes; ++x) most = fmaxf(most, weights[slot + x].m);
+                const float own_f = under(w.m, most);
+                w = Weights{most, w.l * own_f, w.exact * own_f};
+                v *= own_f;
                 for (int x = 1; x < stripes; ++x) {
-                    const float f = under(maxima[slot + x], most);
+                    const float f = under(weights[slot + x].m, most);
                     v += sums[slot + x][at] * f;
-                    l += weights[slot + x] * f;
+                    w.l += weights[slot + x].l * f;
+                    w.exact += weights[slot + x].exact * f;
                 }
-                m = most;
             }
             __syncthreads();
         }
         if (in && stripe == 0)
-            write_values<DT>(a, out_row(cut.row0, group, a.heads, head, (uint32_t)cut.tile * R + r), D, at * 4, v, m, l);
+            write_values<DT>(a, out_row(cut.row0, group, a.heads, head, (uint32_t)cut.tile * R + r), D, at * 4, v, w);
     }
 }
 
@@ -886,7 +915,7 @@ constexpr unsigned attention_groups(size_t kv)
 template <int DT, int NB, int QT, Share SH>
 constexpr size_t attention_bytes(size_t kv)
 {
-    return attention_groups<DT, NB, QT>(kv) * (sizeof(Cut) + 2 * kTileRows<QT, SH> * (32 * NB + 2) * sizeof(float));
+    return attention_groups<DT, NB, QT>(kv) * (sizeof(Cut) + 2 * kTileRows<QT, SH> * (32 * NB + 3) * sizeof(float));
 }
 
 template <int DT, int NB, int QT, Share SH>
