@@ -363,12 +363,16 @@ rc_status rc_mxfp4_cache_read(const rc_cache *cache, size_t tokens, rc_dtype t, 
  * over the tokens j that the row sees: those that are there (a length and a page
  * tell), and if `causal` j <= p, the row's own position, and if window > 0 (causal
  * only, else RC_ERR_UNSUPPORTED) j > p - window.  out: dense, of type t; lse:
- * tokens x heads fp32 values, or NULL.  A row that sees nothing, or only scores of
- * minus infinity, gets out = 0 and lse = -infinity.  What the cache holds where a
- * row does not see does not reach the row, whatever its bytes are; a value that is
- * not finite where it sees makes the row's values of that block of 32 not finite, a
- * score that is not makes all of them so.
- * Scores and sums are FP32.  Rounding: the weights exp(s_j - max) are multiplied as
+ * tokens x heads fp32 values, or NULL.  A row that sees nothing gets out = 0 and
+ * lse = -infinity.  What the cache holds where a row does not see does not reach the
+ * row, whatever its bytes are.  Where it sees, a value that is not finite makes the
+ * row's value in its place not finite and may make the others of that block of 32 so;
+ * a key or query that is not finite gives a score of plus infinity or NaN, which makes
+ * all of the row's values and its lse not finite, or of minus infinity, whose weight
+ * is 0 (a row that has no other score is like one that sees nothing).  Which of them
+ * an infinite key gives is not specified: queries are multiplied in terms.
+ * Scores and sums are FP32; a sum of weights of up to 2^8 times values that passes
+ * 2^128 is infinite.  Rounding: the weights exp(s_j - max) are multiplied as
  * bfloat16 (t bf16, relative 2^-8), or as two (fp16) or three (fp32) terms of it
  * that hold 16 and 24 bits, and below 2^-126 may count as zero; fp32 queries count as the nearest multiple of 2^-133.
  * out is divided by the sum of the weights so rounded; lse is the logarithm of the sum of
