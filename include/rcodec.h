@@ -380,7 +380,8 @@ rc_status rc_mxfp4_cache_read(const rc_cache *cache, size_t tokens, rc_dtype t, 
  * max_query: no sequence has more rows than this, 0 if not known: a hint that the
  * choice of kernels goes by, results are right whatever it says.
  * workspace: rc_mxfp4_cache_attention_workspace(tokens, heads, kv_heads, d) bytes,
- * 16-byte aligned, written before it is read, for one call at a time.  Calls repeat bit for bit. */
+ * 16-byte aligned, written before it is read, for one call at a time; the function
+ * returns 0 for heads, kv_heads and d that the call refuses.  Calls repeat bit for bit. */
 size_t rc_mxfp4_cache_attention_workspace(size_t tokens, size_t heads, size_t kv_heads, size_t d);
 rc_status rc_mxfp4_cache_attention(const rc_cache *cache, rc_dtype t, size_t tokens, size_t heads, const void *q,
                                    size_t q_stride, float scale, int causal, size_t window, size_t max_query,

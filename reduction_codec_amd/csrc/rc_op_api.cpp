@@ -200,7 +200,7 @@ rc_status rc_mxfp4_cache_read(const rc_cache* cache, size_t tokens, rc_dtype t, 
 
 size_t rc_mxfp4_cache_attention_workspace(size_t tokens, size_t heads, size_t kv_heads, size_t d)
 {
-    if (kv_heads == 0 || heads > 65535 || heads % kv_heads != 0 || d > 256) return 0;
+    if (kv_heads == 0 || heads == 0 || heads > 65535 || heads % kv_heads != 0 || d > 256) return 0;
     return rc::cache_attention_work(tokens, heads, kv_heads, d);
 }
 
