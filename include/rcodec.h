@@ -362,8 +362,9 @@ rc_status rc_mxfp4_cache_read(const rc_cache *cache, size_t tokens, rc_dtype t, 
  *   lse = log sum_j exp(s_j)
  * over the tokens j that the row sees: those that are there (a length and a page
  * tell), and if `causal` j <= p, the row's own position, and if window > 0 (causal
- * only, else RC_ERR_UNSUPPORTED) j > p - window.  out: dense, of type t; lse:
- * tokens x heads fp32 values, or NULL.  A row that sees nothing gets out = 0 and
+ * only, else RC_ERR_UNSUPPORTED) j > p - window.  out: dense, of type t, q itself if
+ * that is dense (else RC_ERR_UNSUPPORTED), no other overlap; lse: tokens x heads fp32
+ * values, or NULL.  A row that sees nothing gets out = 0 and
  * lse = -infinity.  What the cache holds where a row does not see does not reach the
  * row, whatever its bytes are.  Where it sees, a value that is not finite makes the
  * row's value in its place not finite and may make the others of that block of 32 so;

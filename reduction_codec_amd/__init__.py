@@ -763,7 +763,7 @@ def mxfp4_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     s, and see what is at or before them (`causal`), the last `window` of that
     if window > 0.  scale: 1 / sqrt(d) by default.  max_query: the most rows a
     sequence has, if known (it only helps to choose the kernel).  Returns out
-    (like q, dense), or (out, the fp32 log-sum-exp of tokens x heads).  See
+    (like q, dense; out=q if q is), or (out, the fp32 log-sum-exp of tokens x heads).  See
     rc_mxfp4_cache_attention."""
     _check_dev(k_cache, "k_cache")
     dev = k_cache.device

@@ -216,6 +216,9 @@ rc_status rc_mxfp4_cache_attention(const rc_cache* cache, rc_dtype t, size_t tok
     if (tokens == 0 || cache->seqs == 0) return RC_OK;
     if (!stride_ok(q_stride, heads * cache->d, t)) return RC_ERR_RANGE;
     if (!q || !out || !workspace) return RC_ERR_NULL;
+    // in place: a tile's rows are read by the workgroup that writes them, or all before the joining kernel does;
+    // rows of another stride would be written over others' that are yet to be read
+    if (out == q && tokens > 1 && q_stride != heads * cache->d) return RC_ERR_UNSUPPORTED;
     s = cache_pointers(*cache);
     if (s != RC_OK) return s;
     if (!aligned16(q) || !aligned16(out) || !aligned(lse, 4) || !aligned16(workspace)) return RC_ERR_ALIGN;
