@@ -31,7 +31,7 @@ class Rank:
     """heads and kv_heads of width d, weights and cache of one rank."""
 
     def __init__(self, width, heads, kv_heads, d, pages, page, device, generator):
-        self.heads, self.kv_heads, self.d = heads, kv_heads, d
+        self.heads, self.kv_heads, self.d, self.page = heads, kv_heads, d, page
         self.all = heads + 2 * kv_heads
         weights = lambda n, k: rca.quantize_pack(  # noqa: E731
             (torch.randn(n, k, device=device, generator=generator) * k ** -0.5).to(torch.bfloat16), rca.MXFP4)
@@ -42,8 +42,8 @@ class Rank:
         qkv = rca.mxfp4_grouped_matmul(x, self.qkv, rows, self.all * self.d).view(-1, self.all, self.d)
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
         place = self.k_cache, self.v_cache, *state
-        q = rca.mxfp4_cache_append(k, v, *place, q=q, rotation=rotation)
-        y = rca.mxfp4_cache_attention(q, *place, max_query=most)
+        q = rca.mxfp4_cache_append(k, v, *place, q=q, rotation=rotation, page=self.page)
+        y = rca.mxfp4_cache_attention(q, *place, max_query=most, page=self.page)
         return rca.mxfp4_grouped_matmul(y.view(y.shape[0], -1), self.out, rows, x.shape[1])
 
 

@@ -659,8 +659,10 @@ def mxfp4_cache_new(pages: int, kv_heads: int, page: int, d: int, device):
     return torch.zeros(shape, dtype=torch.uint8, device=device), torch.zeros(shape, dtype=torch.uint8, device=device)
 
 
-def _cache(k_cache, v_cache, table, lengths, offsets, d: int) -> array.array:
-    """rc_cache of checked tensors, as its eleven 64-bit words."""
+def _cache(k_cache, v_cache, table, lengths, offsets, d: int, page: int | None) -> array.array:
+    """rc_cache of checked tensors, as its eleven 64-bit words.  The bytes of a
+    page tell page * d alone, so a d that is not the cache's is seen only
+    beside the page that the caller names."""
     _check_dev(k_cache, "k_cache")
     index = k_cache.get_device()
     for name, t in (("v_cache", v_cache), ("table", table), ("lengths", lengths), ("offsets", offsets)):
@@ -676,9 +678,11 @@ def _cache(k_cache, v_cache, table, lengths, offsets, d: int) -> array.array:
     if lengths.dim() != 1 or offsets.dim() != 1 or offsets.numel() != seqs + 1 or table.dim() != 2 or \
             table.shape[0] != seqs:
         raise ValueError("need table (sequences x pages), lengths (sequences) and offsets (sequences + 1)")
-    return array.array("Q", (k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[2] // MXFP4_TILE_BYTES * TILE // d,
-                             shape[1], d, table.data_ptr(), seqs, table.shape[1], lengths.data_ptr(),
-                             offsets.data_ptr()))
+    tokens = shape[2] // MXFP4_TILE_BYTES * TILE // d
+    if page is not None and page != tokens:
+        raise ValueError(f"a page of the cache holds {tokens} tokens of {d} values, not {page}")
+    return array.array("Q", (k_cache.data_ptr(), v_cache.data_ptr(), shape[0], tokens, shape[1], d,
+                             table.data_ptr(), seqs, table.shape[1], lengths.data_ptr(), offsets.data_ptr()))
 
 
 def _head_rows(t: torch.Tensor, name: str, index: int):
@@ -700,7 +704,7 @@ def _head_rows(t: torch.Tensor, name: str, index: int):
 def mxfp4_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                        table: torch.Tensor, lengths: torch.Tensor, offsets: torch.Tensor,
                        q: torch.Tensor | None = None, rotation: torch.Tensor | None = None,
-                       interleaved: bool = False, q_out: torch.Tensor | None = None, stream=None):
+                       interleaved: bool = False, q_out: torch.Tensor | None = None, stream=None, page: int | None = None):
     """Write new tokens' keys and values (tokens x kv_heads x d) to the cache,
     keys turned by their positions, and return the queries (tokens x heads x d)
     turned alike, or None without q.  Rows offsets[s] to offsets[s + 1] are the
@@ -712,13 +716,14 @@ def mxfp4_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, 
         rotation = torch.cat([angle.cos(), angle.sin()], 1).float()             # positions x r
 
     turning pairs (i, i + r/2) of the first r values of a head, or (2i, 2i + 1)
-    if `interleaved`.  k, v and q may be parts of one wider tensor.  See
-    rc_mxfp4_cache_append."""
+    if `interleaved`.  k, v and q may be parts of one wider tensor.  page: the
+    tokens of a page, if given checked against the cache and k's width (another
+    width would otherwise be taken for other pages).  See rc_mxfp4_cache_append."""
     _check_dev(k_cache, "k_cache")
     dev, index = k_cache.device, k_cache.get_device()
     tokens, kv_heads, d, k_stride = _head_rows(k, "k", index)
     vt, vh, vd, v_stride = _head_rows(v, "v", index)
-    cache = _cache(k_cache, v_cache, table, lengths, offsets, d)
+    cache = _cache(k_cache, v_cache, table, lengths, offsets, d, page)
     if (vt, vh, vd) != (tokens, kv_heads, d) or v.dtype != k.dtype or kv_heads != k_cache.shape[1]:
         raise ValueError("k and v must have one shape and dtype, and the cache's heads")
     t, heads, q_stride, positions, rot = _dtype(k.dtype, "k"), 0, 0, 0, 0
@@ -740,12 +745,12 @@ def mxfp4_cache_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, 
 
 def mxfp4_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor,
                      offsets: torch.Tensor, tokens: int, d: int, dtype: torch.dtype = torch.bfloat16,
-                     k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None):
+                     k: torch.Tensor | None = None, v: torch.Tensor | None = None, stream=None, page: int | None = None):
     """(k, v), tokens x kv_heads x d each: the rows' keys and values as the
     cache holds them, decoded; rows offsets[s] to offsets[s + 1] are the last
-    tokens of sequence s (all of them if offsets are the lengths' sums).  See
-    rc_mxfp4_cache_read."""
-    cache = _cache(k_cache, v_cache, table, lengths, offsets, d)
+    tokens of sequence s (all of them if offsets are the lengths' sums).  page:
+    as above.  See rc_mxfp4_cache_read."""
+    cache = _cache(k_cache, v_cache, table, lengths, offsets, d, page)
     dev = k_cache.device
     t, shape = _dtype(dtype, "output"), (tokens, k_cache.shape[1], d)
     k, v = _result(k, shape, dtype, dev, stream, "k"), _result(v, shape, dtype, dev, stream, "v")
@@ -756,19 +761,19 @@ def mxfp4_cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.
 def mxfp4_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, table: torch.Tensor,
                           lengths: torch.Tensor, offsets: torch.Tensor, scale: float | None = None,
                           causal: bool = True, window: int = 0, max_query: int | None = None, lse: bool = False,
-                          out: torch.Tensor | None = None, stream=None):
+                          out: torch.Tensor | None = None, stream=None, page: int | None = None):
     """Attention of the queries (tokens x heads x d, heads a multiple of the
     cache's) over their sequences' tokens in the cache, the new ones included:
     rows offsets[s] to offsets[s + 1] stand at the last positions of sequence
     s, and see what is at or before them (`causal`), the last `window` of that
     if window > 0.  scale: 1 / sqrt(d) by default.  max_query: the most rows a
-    sequence has, if known (it only helps to choose the kernel).  Returns out
+    sequence has, if known (it only helps to choose the kernel).  page: as above.  Returns out
     (like q, dense; out=q if q is), or (out, the fp32 log-sum-exp of tokens x heads).  See
     rc_mxfp4_cache_attention."""
     _check_dev(k_cache, "k_cache")
     dev = k_cache.device
     tokens, heads, d, q_stride = _head_rows(q, "q", k_cache.get_device())
-    cache = _cache(k_cache, v_cache, table, lengths, offsets, d)
+    cache = _cache(k_cache, v_cache, table, lengths, offsets, d, page)
     if window < 0 or (max_query is not None and max_query < 0):
         raise ValueError("window and max_query must not be negative")
     t = _dtype(q.dtype, "q")
