@@ -653,8 +653,12 @@ def mxfp4_cache_new(pages: int, kv_heads: int, page: int, d: int, device):
     """(k_cache, v_cache) with room for `pages` pages of `page` tokens, all
     zeros: uint8 tensors pages x kv_heads x bytes, where the last dimension is
     the packed stream {MXFP4, E8M0, 32} of one head's page * d values."""
+    if d not in (64, 96, 128, 192, 256) or not 16 <= page <= 65536 or page & (page - 1):
+        raise ValueError("d must be 64, 96, 128, 192 or 256, and page a power of two from 16 to 65536")
     if page * d % TILE != 0:
         raise ValueError("page * d must be a multiple of 2048")
+    if pages < 0 or kv_heads < 1:
+        raise ValueError("pages must not be negative, and kv_heads at least 1")
     shape = (pages, kv_heads, page * d // TILE * MXFP4_TILE_BYTES)
     return torch.zeros(shape, dtype=torch.uint8, device=device), torch.zeros(shape, dtype=torch.uint8, device=device)
 

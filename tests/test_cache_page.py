@@ -46,3 +46,19 @@ def test_on_the_gpu():
     for call in calls(dev, 64, PAGE) + calls(dev, D, 16):
         with pytest.raises(ValueError, match="a page of the cache holds"):
             call()
+
+
+@pytest.mark.parametrize("pages,kv,page,d", [(4, 2, 8, 256), (4, 2, 48, 128), (4, 2, 1, 2048), (4, 2, 131072, 64), (4, 2, 0, 64),
+                                             (4, 2, 64, 32), (4, 2, 256, 80), (4, 2, 32, 0), (4, 2, 16, 64), (4, 0, 32, 64),
+                                             (-1, 2, 32, 64)])
+def test_no_cache_that_the_calls_would_refuse_is_made(pages, kv, page, d):
+    with pytest.raises(ValueError):
+        rca.mxfp4_cache_new(pages, kv, page, d, "cpu")
+
+
+@pytest.mark.parametrize("d,least", [(64, 32), (96, 64), (128, 16), (192, 32), (256, 16)])
+def test_caches_of_every_width(d, least):
+    for page in (least, 2 * least, 4096):
+        k, v = rca.mxfp4_cache_new(2, 3, page, d, "cpu")
+        assert k.shape == v.shape == (2, 3, page * d // 2048 * 1088) and not k.any()
+    assert rca.mxfp4_cache_new(0, 3, least, d, "cpu")[0].shape[0] == 0
