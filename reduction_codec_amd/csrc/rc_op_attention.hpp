@@ -24,6 +24,7 @@
 
 #include "rc_op_cache.hpp"
 #include "rc_op_matrix.hpp"
+#include "rc_op_rules.hpp"
 
 namespace rc {
 
@@ -933,14 +934,6 @@ hipError_t attention_launch(const CacheAttention& a, float* work, size_t least, 
     return hipGetLastError();
 }
 
-// Rows of a sequence up to which the waves share its tokens, in tiles of 32 (of 16
-// if there are no more rows: one token of 64 sequences of 16000, 181 us, in tiles
-// of 32 194): tiles of 128 rows leave waves without any, and a batch needs both
-// kernels.  Heads of 128 on a quarter of them, bf16, us sharing tokens and rows: 16
-// sequences of 4000, 32 rows 35 and 52, 64 rows 47 and 62, 128 rows 67 and 75; 4 of
-// 30000, 64 rows 70 and 104, 128 rows 115 and 132.
-constexpr size_t kFewRows = 128;
-
 // `rows`: no sequence has more rows of q a head.
 template <int DT, int NB>
 hipError_t attention_d(const CacheAttention& a, size_t rows, hipStream_t st)
@@ -948,10 +941,11 @@ hipError_t attention_d(const CacheAttention& a, size_t rows, hipStream_t st)
     const size_t all = ~(size_t)0;
     Parts first = {}, second = {};
     hipError_t e;
-    if (rows <= 16) e = attention_launch<DT, NB, 1, Share::kTokens>(a, a.work, 0, all, first, st);
-    else if (rows <= kFewRows) e = attention_launch<DT, NB, 2, Share::kTokens>(a, a.work, 0, all, first, st);
-    else if (a.c.seqs == 1) e = attention_launch<DT, NB, 2, Share::kRows>(a, a.work, 0, all, first, st);
-    else {
+    switch (attention_form(rows, a.c.seqs)) {
+    case AttentionForm::kTokens16: e = attention_launch<DT, NB, 1, Share::kTokens>(a, a.work, 0, all, first, st); break;
+    case AttentionForm::kTokens32: e = attention_launch<DT, NB, 2, Share::kTokens>(a, a.work, 0, all, first, st); break;
+    case AttentionForm::kRows: e = attention_launch<DT, NB, 2, Share::kRows>(a, a.work, 0, all, first, st); break;
+    default:
         e = attention_launch<DT, NB, 2, Share::kRows>(a, a.work, kFewRows, all, first, st);
         if (e != hipSuccess) return e;
         float* const behind = a.work + attention_bytes<DT, NB, 2, Share::kRows>(a.c.kv_heads) / 4;

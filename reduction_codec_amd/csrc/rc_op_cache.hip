@@ -9,6 +9,7 @@
 // maximum, and what 21 bits of x drop is kept as their last bit, from where the
 // rounding to four bits goes the way that the value itself would.
 #include "rc_op_cache.hpp"
+#include "rc_op_rules.hpp"
 
 namespace rc {
 namespace {
@@ -61,14 +62,8 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v)
     return v > o ? v : o;
 }
 
-// Lanes of a workgroup where units go one by one, and where it takes a token.
-// Every wave looks its token up, so a token has few: 12288 tokens of 48 heads of
-// 128 in bf16 are appended in 55 us by two waves (76 by four, 60 by one, against
-// 59, before values were loaded past the caches).  But fewer than kFewTokens
-// tokens leave the card empty, so their heads are cut as well: 64 tokens 3.7 us
-// cut and 5.0 whole, 768 tokens 7.7 and 8.0, 1536 tokens 11.8 and 11.4; read back
-// 2.8 and 3.0, 3.7 and 3.9, 4.8 and 5.2, 12288 16.9 and 15.2.
-constexpr int kAppendLanes = 256, kTokenLanes = 128, kFewTokens = 1024;
+// Lanes of a workgroup where units go one by one; kTokenLanes where it takes a token.
+constexpr int kAppendLanes = 256;
 
 // The upper half of |y| with its last bit set where the lower half holds
 // anything: 21 bits, from where any rounding to 19 or fewer is right.
@@ -325,10 +320,8 @@ template <int DT, int D>
 hipError_t append_t(const CacheAppend& a, hipStream_t st)
 {
     if constexpr (D % 64 == 0) {
-        if (a.rot % 64 == 0 || a.interleaved) {
-            // few tokens: their heads side by side
-            constexpr unsigned HP = kTokenLanes / (D / 16);
-            const unsigned turns = ((unsigned)(a.heads + 2 * a.c.kv_heads) + HP - 1) / HP, y = a.c.tokens < kFewTokens ? turns : 1;
+        if (append_in_pairs(D, (unsigned)a.rot, a.interleaved)) {
+            const unsigned y = side_by_side(a.c.tokens, append_turns((unsigned)(a.heads + 2 * a.c.kv_heads), D));
             cache_append_pairs_kernel<DT, D><<<grid_of_tokens(a.c.tokens, y), kTokenLanes, 0, st>>>(a);
             return hipGetLastError();
         }
@@ -341,7 +334,7 @@ hipError_t append_t(const CacheAppend& a, hipStream_t st)
 template <int DT, int D>
 hipError_t read_t(const Cache& c, void* k, void* v, hipStream_t st)
 {
-    const unsigned turns = ((unsigned)c.kv_heads * 2 * (D / 8) + kTokenLanes - 1) / kTokenLanes, y = c.tokens < kFewTokens ? turns : 1;
+    const unsigned y = side_by_side(c.tokens, read_turns((unsigned)c.kv_heads, D));
     cache_read_kernel<DT, D><<<grid_of_tokens(c.tokens, y), kTokenLanes, 0, st>>>(c, k, v);
     return hipGetLastError();
 }

@@ -1,5 +1,6 @@
-// rc_op_rules.hpp -- which kernel a product grouped by expert takes: rules on
-// sizes and types alone, without HIP, so that a host program can ask them too.
+// rc_op_rules.hpp -- which kernel a product grouped by expert or a call on a paged
+// cache takes: rules on sizes and types alone, without HIP, so that a host program
+// can ask them too.
 #pragma once
 
 #include <algorithm>
@@ -83,5 +84,39 @@ inline Dw dw_form(bool f32, const GroupedSizes& s)
     if (f32) return Dw::k128x128F32;
     return (size_t)((s.n + 255) / 256) * (size_t)((s.k + 255) / 256) * s.experts < 512 ? Dw::k128x128 : Dw::k256x256;
 }
+
+// Attention over a cache.  Rows of a sequence up to which the waves share its
+// tokens, in tiles of 32 (of 16 if there are no more rows: one token of 64
+// sequences of 16000, 181 us, in tiles of 32 194): tiles of 128 rows leave waves
+// without any, and a batch of which some may have more needs both kernels, each for
+// the sequences of its kind.  Heads of 128 on a quarter of them, bf16, us sharing
+// tokens and rows: 16 sequences of 4000, 32 rows 35 and 52, 64 rows 47 and 62, 128
+// rows 67 and 75; 4 of 30000, 64 rows 70 and 104, 128 rows 115 and 132.
+constexpr size_t kFewRows = 128;
+enum class AttentionForm : int { kTokens16, kTokens32, kRows, kBoth };
+
+// `rows`: no sequence has more rows of q a head of the cache.
+inline AttentionForm attention_form(size_t rows, size_t seqs)
+{
+    if (rows <= 16) return AttentionForm::kTokens16;
+    if (rows <= kFewRows) return AttentionForm::kTokens32;
+    return seqs == 1 ? AttentionForm::kRows : AttentionForm::kBoth;
+}
+
+// Appending to a cache and reading it.  Every wave looks its token up, so a token
+// has few lanes: 12288 tokens of 48 heads of 128 in bf16 are appended in 55 us by
+// two waves (76 by four, 60 by one, against 59, before values were loaded past the
+// caches).  But fewer than kFewTokens tokens leave the card empty, so the `turns`
+// that a workgroup takes over its heads are workgroups of their own: 64 tokens 3.7
+// us so and 5.0 one after another, 768 tokens 7.7 and 8.0, 1536 tokens 11.8 and
+// 11.4; read back 2.8 and 3.0, 3.7 and 3.9, 4.8 and 5.2, 12288 16.9 and 15.2.
+constexpr unsigned kTokenLanes = 128;
+constexpr size_t kFewTokens = 1024;
+inline unsigned append_turns(unsigned rows, unsigned d) { const unsigned at_once = kTokenLanes / (d / 16); return (rows + at_once - 1) / at_once; }
+inline unsigned read_turns(unsigned kv_heads, unsigned d) { return (2 * kv_heads * (d / 8) + kTokenLanes - 1) / kTokenLanes; }
+inline unsigned side_by_side(size_t tokens, unsigned turns) { return tokens < kFewTokens ? turns : 1; }
+
+// Appending takes whole pairs of units where a block's units are in neighbouring lanes.
+inline bool append_in_pairs(unsigned d, unsigned rot, bool interleaved) { return d % 64 == 0 && (rot % 64 == 0 || interleaved); }
 
 }  // namespace rc
