@@ -72,9 +72,13 @@ class Block:
 
 def serve(steps=32, prompts=(700, 64, 1500, 200), ranks=2, width=1024, heads=16, kv_heads=4, d=64, page=64, seed=0, log=print):
     """Outputs of the prompts' rows and of every step's."""
+    if ranks < 1 or heads % ranks or kv_heads % ranks:
+        raise ValueError(f"{heads} heads on {kv_heads} of the cache cannot be shared by {ranks} ranks alike")
+    if min(prompts, default=0) < 1:
+        raise ValueError("every sequence needs a prompt of one token at least")
     device = torch.device("cuda:0")
     g = torch.Generator(device=device).manual_seed(seed)
-    block = Block(width, heads, kv_heads, d, ranks, prompts, steps, page, device, g)
+    block = Block(width, heads, kv_heads, d, ranks, prompts, max(steps, 1), page, device, g)   # (the first call takes a row)
     randn = lambda n: torch.randn(n, width, device=device, generator=g).to(torch.bfloat16)  # noqa: E731
     i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=device)  # noqa: E731
 
