@@ -786,6 +786,6 @@ def mxfp4_cache_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     ws = _result(None, ((_lib or lib()).rc_mxfp4_cache_attention_workspace(tokens, heads, k_cache.shape[1], d),),
                  torch.uint8, dev, stream, "")
     _launch("rc_mxfp4_cache_attention", dev, stream, cache.buffer_info()[0], t, tokens, heads, q.data_ptr(), q_stride,
-            d ** -0.5 if scale is None else scale, int(causal), window, max_query or 0, out.data_ptr(), _ptr(sums),
+            d ** -0.5 if scale is None else scale, int(causal), min(window, 1 << 32), max_query or 0, out.data_ptr(), _ptr(sums),
             ws.data_ptr())
     return (out, sums) if lse else out

@@ -62,3 +62,14 @@ def test_caches_of_every_width(d, least):
         k, v = rca.mxfp4_cache_new(2, 3, page, d, "cpu")
         assert k.shape == v.shape == (2, 3, page * d // 2048 * 1088) and not k.any()
     assert rca.mxfp4_cache_new(0, 3, least, d, "cpu")[0].shape[0] == 0
+
+
+def test_a_window_past_64_bits_is_no_window(on_the_cpu, monkeypatch):
+    """Positions end at 2^30: the library is handed no more than it can hold."""
+    seen = []
+    monkeypatch.setattr(rca, "_launch", lambda what, dev, stream, *args: seen.append(args[8]))
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    place = (*rca.mxfp4_cache_new(3, KV, PAGE, D, "cpu"), i32([[1, 2]]), i32([40]), i32([0, 2]))
+    for window in (0, 5, 1 << 31, (1 << 64) + 5):
+        rca.mxfp4_cache_attention(torch.ones(2, KV, D), *place, window=window)
+    assert seen[:2] == [0, 5] and all((1 << 30) < w < (1 << 64) for w in seen[2:])
