@@ -53,3 +53,13 @@ def test_windows_and_every_row_seeing_all():
     for spec, most in ((DECODE, 1), (MIXED, None), (MIXED, 170)):
         check(ref.Plan(spec, 16), 4, 2, 128, torch.bfloat16, window=37, most=most)
         check(ref.Plan(spec, 16), 4, 2, 128, torch.bfloat16, causal=False, most=most)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("spec", [DECODE, MIXED, LONG], ids=["one", "mixed", "long"])
+def test_values_are_the_same_without_it(dtype, spec):
+    plan = ref.Plan(spec, 16)
+    cache = [c.to(DEV) for c in ref.random_cache(plan, 2, 128, 1)[:2]]
+    q = torch.randn(plan.tokens, 4, 128, generator=torch.Generator().manual_seed(2)).to(dtype).to(DEV)
+    out, _ = rca.mxfp4_cache_attention(q, *cache, *plan.tensors(DEV), lse=True)
+    assert torch.equal(out, rca.mxfp4_cache_attention(q, *cache, *plan.tensors(DEV)))
