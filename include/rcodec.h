@@ -338,7 +338,7 @@ typedef struct {
  * Rows of k, v and q are k_stride, v_stride and q_stride elements apart (a fused
  * projection's parts are taken where they lie), multiples of 16 bytes, at least a
  * row's length and at most 2^31 bytes; q_out is dense.  rotation: `positions` >=
- * max_pages * page rows of `rot` values, NULL or rot = 0 for none; rot is a
+ * max_pages * page rows of `rot` values, one at least, NULL or rot = 0 for none; rot is a
  * multiple of 16, at most d.  heads is a multiple of kv_heads, at most 65535, or 0
  * without q.  A token whose position is negative or whose page does not exist is
  * not written to the cache; its query is turned by position 0 if the position is

@@ -172,7 +172,8 @@ rc_status rc_mxfp4_cache_append(const rc_cache* cache, rc_dtype t, size_t tokens
     if (s != RC_OK) return s;
     const size_t d = cache->d, kv = cache->kv_heads;
     if (heads > 65535 || heads % kv != 0 || rot % 16 != 0 || rot > d) return RC_ERR_RANGE;
-    if (rotation && rot != 0 && positions < cache->max_pages * cache->page) return RC_ERR_RANGE;
+    // (rows before the first position take the first angles, which a table without columns needs too)
+    if (rotation && rot != 0 && (positions == 0 || positions < cache->max_pages * cache->page)) return RC_ERR_RANGE;
     if (tokens == 0 || cache->seqs == 0) return RC_OK;
     if (!stride_ok(k_stride, kv * d, t) || !stride_ok(v_stride, kv * d, t) || (heads != 0 && !stride_ok(q_stride, heads * d, t))) return RC_ERR_RANGE;
     if (q_out == q && q != nullptr && heads != 0) return RC_ERR_UNSUPPORTED;
