@@ -311,7 +311,7 @@ rc_status rc_grad_norm_clip(const rc_grad *grads, size_t count, float scale, flo
  * graph follows them) and left alone while a call runs; what they hold cannot lead outside the buffers:
  * lengths count as at least 0 and at most max_pages * page, offsets are clamped to
  * the rows there are, and pages outside [0, pages) hold no token.
- * Offsets that do not ascend give unspecified results.  Rows that belong to no
+ * Offsets that do not ascend give unspecified results but no access outside the buffers.  Rows that belong to no
  * sequence (before offsets[0], from offsets[seqs] on) are neither read nor written.
  * d is 64, 96, 128, 192 or 256; page a power of two from 16 to 65536 with page * d
  * a multiple of 2048; kv_heads and seqs at most 65535; pages and tokens

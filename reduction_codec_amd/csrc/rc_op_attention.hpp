@@ -270,13 +270,21 @@ __device__ __forceinline__ Tiles tiles_of(const CacheAttention& a, const Sequenc
     return {n, (n + 1) / 2, u};
 }
 
-// Sequence s if it is one of those with `least` < rows <= `most`.
+// Units of all sequences are at most 2^51: bounds that ascend give 2^31 rows, so
+// 2^27 + 2^16 tiles, of pairs of up to 2^24 + 4 units.  Bounds that do not would give each
+// sequence as many, past 64 bits; one that is below its predecessor counts as
+// kDisorder units, and a launch that finds more than kMostUnits does nothing.
+// (128 sequences at once, and 256 to a lane of a workgroup, stay below 2^61.)
+constexpr int64_t kMostUnits = (int64_t)1 << 52, kDisorder = (int64_t)1 << 53;
+
+// Sequence s if it is one of those with `least` < rows <= `most`; tokens -1 if its bounds are out of order.
 __device__ __forceinline__ Sequence sequence(const CacheAttention& a, int s, uint32_t group, uint32_t least, uint32_t most)
 {
     Sequence q = {0, 0, 0};
     if (s >= a.c.seqs) return q;
     const int lo = clamp_to(a.c.offsets[s], a.c.tokens), hi = clamp_to(a.c.offsets[s + 1], a.c.tokens);
-    const uint32_t rows = hi > lo ? (uint32_t)(hi - lo) * group : 0;
+    if (hi < lo) return {0, -1, 0};
+    const uint32_t rows = (uint32_t)(hi - lo) * group;
     if (rows <= least || rows > most) return q;
     return {lo, hi - lo, a.c.pages == 0 ? 0 : seq_length(a.c, s)};
 }
@@ -380,7 +388,8 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
     const unsigned worker = xcd * (groups / 8) + (xcd < left ? xcd : left) + blockIdx.x / 8;
     const int range = worker / kv, head = worker % kv, most_ranges = groups / kv;
 
-    const auto units_of = [&](const Sequence& q) {
+    const auto units_of = [&](const Sequence& q) -> int64_t {
+        if (q.tokens < 0) return kDisorder;
         const Tiles t = tiles_of<R>(a, q, group);
         return t.units * t.pairs;
     };
@@ -414,6 +423,7 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
     if (a.c.seqs > kSeqs) {
         int64_t rest = 0;
         for (int s = kSeqs + (int)tid; s < a.c.seqs; s += T) rest += units_of(sequence(a, s, group, least, most_rows));
+        rest = rest < kDisorder ? rest : kDisorder;              // (all lanes' sum fits)
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) rest += __shfl_xor(rest, d, 64);
         if (lane == 0) sums[wave] = rest;
@@ -421,7 +431,7 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
 #pragma unroll
         for (int w = 0; w < kRowWaves; ++w) total += sums[w];
     }
-    const int64_t ranges = total < most_ranges ? total : most_ranges;
+    const int64_t ranges = total > kMostUnits ? 0 : total < most_ranges ? total : most_ranges;
     Cut* const cuts = reinterpret_cast<Cut*>(work);
     if (tid == 0) cuts[worker] = Cut{0, 0, 0, 0};
     if (range >= ranges) return;
