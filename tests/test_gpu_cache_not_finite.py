@@ -1,5 +1,6 @@
 """Keys and values that are not finite, in blocks of any codes and scales, under both ways to share a tile: what
 reaches the rows that see them, and that nothing reaches the others; and the smallest scale, 2^-127."""
+import functools
 import math
 
 import pytest
@@ -15,6 +16,21 @@ DEV = torch.device("cuda:0")
 KV, D, BLOCK = 2, 128, 1
 SPEC = [(140, 170), (1, 40), (150, 150)]                     # 140 and 150 rows a head of the cache or more, and one
 HIDDEN = [0, 5, 63, 100, 165]                                # positions of the first sequence, its first and last steps' among them
+
+
+@functools.lru_cache(None)
+def setting(dtype, sign="any"):
+    plan = ref.Plan(SPEC, 16)
+    q = torch.randn(plan.tokens, 4, D, generator=torch.Generator().manual_seed(9)).to(dtype)
+    q = {"any": q, "positive": q.abs(), "negative": -q.abs(), "-1": -torch.ones_like(q)}[sign]
+    return plan, ref.random_cache(plan, KV, D, 5), q
+
+
+@functools.lru_cache(None)
+def clean(dtype, sign="any", window=0, hidden=None):
+    """The plain statement of the cache as it was, and without the first sequence's token `hidden`."""
+    plan, cache, q = setting(dtype, sign)
+    return ref.attention(plan if hidden is None else _Hidden(plan, hidden), q, *cache[2:], D ** -0.5, True, window)
 
 
 def place(c, plan, seq, pos):
@@ -56,10 +72,7 @@ def near(got, out, tol, dtype):
 @pytest.mark.parametrize("byte,first", [(253, 4), (254, 2), (255, 0)])
 def test_a_value_reaches_its_place_in_the_rows_that_see_it_and_its_block_at_most(dtype, most, byte, first):
     """Codes of all magnitudes side by side: under 2^126 those from 4 on are infinite, under 2^127 from 2 on."""
-    plan = ref.Plan(SPEC, 16)
-    cache = ref.random_cache(plan, KV, D, 5)
-    g = torch.Generator().manual_seed(9)
-    q = torch.randn(plan.tokens, 4, D, generator=g).to(dtype)
+    plan, cache, q = setting(dtype)
     codes = torch.tensor([0x10, 0x32, 0x54, 0x76, 0x98, 0xBA, 0xDC, 0xFE] * 2, dtype=torch.uint8)
     for pos, window in [(p, 0) for p in HIDDEN] + [(63, 20)]:
         both, vals = with_block(cache, plan, 1, pos, codes, byte)
@@ -67,7 +80,7 @@ def test_a_value_reaches_its_place_in_the_rows_that_see_it_and_its_block_at_most
         magnitudes = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6] * 4)
         assert torch.equal(bad[32:64], (magnitudes >= first) | (byte == 255)) and bad.sum() == bad[32:64].sum()
         got, lse = answer(plan, q, both, most, window)
-        out, ls, tol, lse_tol = ref.attention(plan, q, cache[2], cache[3], D ** -0.5, True, window)  # of the cache before
+        out, ls, tol, lse_tol = clean(dtype, window=window)
         row = sees(plan, pos, window)
         assert row.any() and not torch.isfinite(got[row][:, :, bad]).any()
         fine = torch.ones_like(got, dtype=torch.bool)
@@ -83,15 +96,11 @@ def test_a_value_reaches_its_place_in_the_rows_that_see_it_and_its_block_at_most
 def test_a_key_spoils_the_rows_that_see_it_or_counts_for_nothing(dtype, most, byte, sign):
     """An infinite key gives scores of either infinity, or NaN: the row's values and lse are not finite, or they are
     those without the key."""
-    plan = ref.Plan(SPEC, 16)
-    cache = ref.random_cache(plan, KV, D, 5)
-    g = torch.Generator().manual_seed(9)
-    q = torch.randn(plan.tokens, 4, D, generator=g).to(dtype)
-    q = {"any": q, "positive": q.abs(), "negative": -q.abs(), "-1": -torch.ones_like(q)}[sign]
+    plan, cache, q = setting(dtype, sign)
     for pos, window in ((5, 0), (100, 0), (63, 20)):
         both, _ = with_block(cache, plan, 0, pos, torch.full((16,), 0x77, dtype=torch.uint8), byte)
         got, lse = answer(plan, q, both, most, window)
-        out, ls, tol, lse_tol = ref.attention(plan, q, cache[2], cache[3], D ** -0.5, True, window)
+        out, ls, tol, lse_tol = clean(dtype, sign, window)
         row = sees(plan, pos, window)
         assert near(got, out, tol, dtype)[~row].all() and ((lse - ls).abs() <= lse_tol)[~row].all()
         spoilt = ~torch.isfinite(got)
@@ -99,7 +108,7 @@ def test_a_key_spoils_the_rows_that_see_it_or_counts_for_nothing(dtype, most, by
             assert spoilt[row].all() and not torch.isfinite(lse[row]).any()
             continue
         assert (spoilt.all(2) == spoilt.any(2)).all() and (spoilt.any(2) == ~torch.isfinite(lse)).all()
-        without = ref.attention(_Hidden(plan, pos), q, cache[2], cache[3], D ** -0.5, True, window)
+        without = clean(dtype, sign, window, pos)
         left = row[:, None] & ~spoilt.any(2)
         assert near(got, without[0], without[2], dtype)[left].all()
         assert ((lse - without[1]).abs() <= without[3])[left].all()
@@ -125,13 +134,9 @@ def test_a_query_that_is_not_finite_stays_in_its_row(dtype, most):
     and this row's score, which no maximum is large enough for, moves theirs at every step. A weight is then formed
     under another maximum m': e^(s - m') rounded, for e^(s - m) rounded and multiplied by e^(m - m') rounded. Both are
     within the roundings that the bound counts for each weight and sum, and need not be the same."""
-    plan = ref.Plan(SPEC, 16)
-    both = ref.random_cache(plan, KV, D, 5)
-    cache = [c.to(DEV) for c in both[:2]]
-    g = torch.Generator().manual_seed(9)
-    q = torch.randn(plan.tokens, 4, D, generator=g).to(dtype)
-    out, ls, tol, lse_tol = ref.attention(plan, q, *both[2:], D ** -0.5)
-    q = q.to(DEV)
+    plan, both, q = setting(dtype)
+    cache, q = [c.to(DEV) for c in both[:2]], q.to(DEV)
+    out, ls, tol, lse_tol = clean(dtype)
     for row in (7, 130, 140, 200):
         for bad in (math.nan, math.inf, -math.inf):
             p = q.clone()
