@@ -358,9 +358,9 @@ constexpr int row_groups(int terms, int nb, int qt)
     return by_regs < by_lds ? by_regs : by_lds;
 }
 
-// Every wave reads and decodes its tokens by itself: keys go from memory to the
-// registers that the matrix instructions read; values pass through LDS, decoded,
-// to be read transposed.
+// Every wave reads and decodes its tokens by itself: keys pass through LDS as
+// codes, from the lanes that asked for them to those that multiply them; values
+// pass through it decoded, to be read transposed.
 template <int DT, int NB, int QT, Share SH>
 __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) void attention_kernel(
     const CacheAttention a, float* work, uint32_t least, uint32_t most_rows)
@@ -369,8 +369,8 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
     constexpr int kSeqs = 128;                   // sequences looked at at a time
     constexpr int kStride = SH == Share::kTokens ? kUnit : 32;       // tokens from a wave's step to its next
     constexpr int kDepth = SH == Share::kTokens && QT == 1 ? 2 : 1;  // steps asked for ahead
-    // kept, addresses would take registers that queries and sums need (16 rows of 256 values: 89 spilled, 24 so), but
-    // where there is room they are better kept (prompts, 32 rows of 128 values: 540 us, 513 so)
+    // kept, addresses would take registers that queries and sums need (16 rows of 256 values: 63 spilled, 20 so), but
+    // where there is room they are better kept (prompts, 32 rows of 128 values: 499 us, 457 so)
     constexpr bool kTight = lane_registers(P, NB, QT) > 230 && lane_registers(P, NB, QT) <= 256;
     constexpr float kLog2e = 1.44269504f;
     constexpr bool kExactSum = P < 3;             // three terms are the weight itself
@@ -577,8 +577,9 @@ __global__ __launch_bounds__(64 * kRowWaves, row_groups(Terms<DT>::v, NB, QT)) v
             }
         };
         // Tiles of rows wait for the matrix cores, two waves a SIMD: one that feeds them goes before one that forms
-        // weights (prompts of 4500 tokens on average, 32 heads of 128: 516 us without, 469 so; chunks 442, 396).  Waves
-        // that share tokens wait for memory: no difference.
+        // weights (prompts of 4500 tokens on average, 32 heads of 128: 508 us without, 457 so; chunks 388, 348; but heads
+        // of 256, whose one wave a SIMD has none to go before, 1004 and 1040).  Waves that share tokens wait for memory:
+        // no difference.
         struct Prefer {
             __device__ __forceinline__ void operator()(int level) const
             {
@@ -919,7 +920,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const CacheAttentio
     }
 }
 
-// Workgroups of a launch: whole ranges of all heads; and its workspace.
+// Workgroups of a launch: whole ranges of all heads, as many as the card's 256
+// units hold (a number of its own, as the workspace is sized without a card), or
+// one range where there are more heads; and its workspace.
 template <int DT, int NB, int QT>
 constexpr unsigned attention_groups(size_t kv)
 {

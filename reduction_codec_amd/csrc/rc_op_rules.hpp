@@ -87,7 +87,7 @@ inline Dw dw_form(bool f32, const GroupedSizes& s)
 
 // Attention over a cache.  Rows of a sequence up to which the waves share its
 // tokens, in tiles of 32 (of 16 if there are no more rows: one token of 64
-// sequences of 16000, 181 us, in tiles of 32 194): tiles of 128 rows leave waves
+// sequences of 16000, 166 us, in tiles of 32 174): tiles of 128 rows leave waves
 // without any, and a batch of which some may have more needs both kernels, each for
 // the sequences of its kind.  Heads of 128 on a quarter of them, bf16, us sharing
 // tokens and rows: 16 sequences of 4000, 32 rows 35 and 52, 64 rows 47 and 62, 128
