@@ -380,8 +380,8 @@ rc_status rc_mxfp4_cache_read(const rc_cache *cache, size_t tokens, rc_dtype t, 
  * the weights before that, FP32 for every type of the queries.
  * max_query: no sequence has more rows than this, 0 if not known: a hint that the
  * choice of kernels goes by, results are right whatever it says.
- * workspace: rc_mxfp4_cache_attention_workspace(tokens, heads, kv_heads, d) bytes (6 to 82 MB
- * up to 256 kv_heads, from some hundreds on up to 324 KB for each of them),
+ * workspace: rc_mxfp4_cache_attention_workspace(tokens, heads, kv_heads, d) bytes (5 to 86 MB
+ * up to 256 kv_heads, from some hundreds on up to 332 KB for each of them),
  * 16-byte aligned, written before it is read, for one call at a time; the function
  * returns 0 for heads, kv_heads and d that the call refuses.  Calls repeat bit for bit. */
 size_t rc_mxfp4_cache_attention_workspace(size_t tokens, size_t heads, size_t kv_heads, size_t d);

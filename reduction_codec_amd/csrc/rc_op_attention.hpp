@@ -17,7 +17,7 @@
 // (fp16) or three (fp32) bfloat16 terms that add up to them, and so are the
 // weights exp(s_j - m).  One term rounds them to half a step of bfloat16, 2^-8 at
 // most of themselves: bf16 results, whose own rounding is as large, are then off by
-// 0.0021 of their norm, 0.0016 with a second term.  That would cost more than it
+// 0.0021 of their norm (normal values), 0.0016 with a second term.  That would cost more than it
 // gives where the matrix cores bound (us with one and two: prompts of 4500 tokens on
 // average 468, 549; chunks behind 30000 359, 439; heads of 256 1038, 1196).
 #pragma once
